@@ -22,6 +22,7 @@ Functions (same names as the C entry points, without the ``spec_`` prefix):
   verify_tree_sample  stochastic tree-walk verification (target draws along the tree)
   kv_compact     keep the accepted path's KV rows
   adaptive_len   DSpark survival, expected advance and verify length
+  cache_*        the paged 4-bit KV cache of the target model (cache.py)
 """
 from __future__ import annotations
 
@@ -590,3 +591,11 @@ def adaptive_len(conf, a: float, b: float, *, cost=None, out: Optional[AdaptiveL
                                         _p(out.l_row_off), _p(out.q_row_off), _stream(stream))
         _check(rc, "spec_adaptive_len_table")
     return out
+
+
+# ---------------------------------------------------------------------------
+# the paged 4-bit cache
+# ---------------------------------------------------------------------------
+from .cache import (ST_BAD_PAGE, ST_NO_PAGE, CacheAttention, PageState, cache_append, cache_attend,  # noqa: E402
+                    cache_block_bytes, cache_compact, cache_fork, cache_read, cache_release, cache_reserve,
+                    page_state)

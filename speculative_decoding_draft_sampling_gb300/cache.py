@@ -1,0 +1,290 @@
+"""The paged 4-bit KV cache that a verification pass reads, writes and cuts
+back (C ABI: include/spec_cache.h).
+
+A pool is a uint8 CUDA tensor [pages, kv_heads, block] for one layer, or
+[layers, pages, kv_heads, block] where a call works on all layers
+(cache_compact, cache_fork); block = cache_block_bytes(head_dim, page_size).
+A block holds one page of P tokens of one kv head:
+
+    K codes [P][D/2] | K scales bf16 [P][D/32] | V codes [P][D/2] | V scales bf16 [P][D/32]
+
+page_table [B, M] int32 names the pages of each request in order (-1: none).
+`status` arguments are optional int32 [B] tensors; bits are OR-ed in.
+
+  cache_append   quantise rows of K and V into the cache
+  cache_read     rows of the cache as bf16 values
+  cache_attend   attention of drafted rows over the cache (chains, ancestor
+                 masks, sliding window with sinks)
+  cache_compact  keep an accepted path's rows, in place
+  cache_reserve, cache_fork, cache_release   pages of growing, forked and
+                 finished requests
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from dataclasses import dataclass
+from typing import Optional
+
+import torch
+
+from . import SpecError, _check, _cuda, _dev, _load, _p, _stream, workspace
+
+ST_BAD_PAGE, ST_NO_PAGE = 128, 256
+
+_bound = None
+
+
+def _lib():
+    global _bound
+    if _bound is None:
+        lib = _load()
+        P, i32, i64, f32, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+        lib.spec_cache_block_bytes.argtypes = [i32, i32]
+        lib.spec_cache_block_bytes.restype = sz
+        lib.spec_cache_attend_workspace_size.argtypes = [i32] * 5
+        lib.spec_cache_attend_workspace_size.restype = sz
+        lib.spec_cache_append.argtypes = [P, i64, i64, i64, P, i64, i64, i64, P, i64, i64, i32, P, i64, i32, P, P,
+                                          i32, i32, i32, i32, i32, P, P]
+        lib.spec_cache_read.argtypes = [P, i64, i64, i32, P, i64, i32, P, P, i32, i32, i32, i32, i32, P, P, P, P]
+        lib.spec_cache_attend.argtypes = [P, i64, i64, i64, P, i64, i64, i32, P, i64, i32, P, P, P, P, i32, i32, f32,
+                                          i32, i32, i32, i32, i32, i32, P, P, P, P, sz, P]
+        lib.spec_cache_compact.argtypes = [P, i32, i64, i64, i64, i32, P, i64, i32, P, P, i32, P,
+                                           i32, i32, i32, i32, P, P]
+        lib.spec_cache_reserve.argtypes = [P, i64, i32, P, P, P, P, i32, P, i32, i32, P, P]
+        lib.spec_cache_release.argtypes = [P, i64, i32, P, P, P, P, i32, P, i32, i32, P, P]
+        lib.spec_cache_fork.argtypes = [P, i32, i64, i64, i64, P, i64, i32, P, P, P, P, i32, P, P, P, i32, i32,
+                                        i32, i32, i32, P, P, P]
+        for name in ("append", "read", "attend", "compact", "reserve", "release", "fork"):
+            getattr(lib, "spec_cache_" + name).restype = i32
+        _bound = lib
+    return _bound
+
+
+def cache_block_bytes(head_dim: int, page_size: int) -> int:
+    """Bytes of one page of one kv head."""
+    n = int(_lib().spec_cache_block_bytes(int(head_dim), int(page_size)))
+    if n == 0:
+        raise SpecError(f"unsupported cache shape: head_dim is 64 or 128 and page_size 16, 32 or 64 "
+                        f"(got {head_dim} and {page_size})")
+    return n
+
+
+def _ints(t, name: str, shape, contiguous: bool = True):
+    _cuda(t, name, torch.int32)
+    if tuple(t.shape) != tuple(shape) or (contiguous and not t.is_contiguous()):
+        raise SpecError(f"{name} must be a contiguous {list(shape)} int32 tensor")
+    return t
+
+
+def _opt_ints(t, name: str, shape):
+    return None if t is None else _ints(t, name, shape)
+
+
+def _pool(pool, dims: int, head_dim: int):
+    """(page_size, kv_heads, num_pages) of a pool of `dims` dimensions."""
+    if not isinstance(pool, torch.Tensor) or not pool.is_cuda or pool.dtype != torch.uint8 or pool.dim() != dims \
+            or pool.stride(-1) != 1:
+        raise SpecError("pool must be a uint8 CUDA tensor "
+                        + ("[pages, kv_heads, block]" if dims == 3 else "[layers, pages, kv_heads, block]")
+                        + " with unit element stride")
+    page = pool.shape[-1] * 8 // (9 * head_dim)
+    if page not in (16, 32, 64) or page * head_dim * 9 // 8 != pool.shape[-1]:
+        raise SpecError(f"a block of {pool.shape[-1]} bytes is no page of head_dim {head_dim}")
+    return page, pool.shape[-2], pool.shape[-3]
+
+
+def _table(page_table, B: Optional[int] = None):
+    _cuda(page_table, "page_table", torch.int32)
+    if page_table.dim() != 2 or page_table.stride(1) != 1 or (B is not None and page_table.shape[0] != B):
+        raise SpecError("page_table must be [B, M] int32 with unit element stride")
+    return page_table.shape
+
+
+def cache_append(k, v, pool, page_table, start, count=None, *, status=None, stream=None) -> None:
+    """Write k, v [B, n, kv_heads, D] bf16 (any strides, unit element stride)
+    into the cache in 4 bits: row (b, i), i < count[b] (default n), at position
+    start[b] + i.  Groups of 32 values share a scale."""
+    L = _lib()
+    _cuda(k, "k", torch.bfloat16)
+    _cuda(v, "v", torch.bfloat16)
+    if k.dim() != 4 or v.shape != k.shape or k.stride(3) != 1 or v.stride(3) != 1:
+        raise SpecError("k and v must be [B, n, kv_heads, D] with unit element stride")
+    B, n, H, D = k.shape
+    page, heads, pages = _pool(pool, 3, D)
+    if heads != H:
+        raise SpecError(f"the pool has {heads} kv heads, k and v {H}")
+    M = _table(page_table, B)[1]
+    _check(L.spec_cache_append(_p(k), k.stride(0), k.stride(1), k.stride(2),
+                               _p(v), v.stride(0), v.stride(1), v.stride(2),
+                               _p(pool), pool.stride(0), pool.stride(1), pages,
+                               _p(page_table), page_table.stride(0), M,
+                               _p(_ints(start, "start", (B,))), _p(_opt_ints(count, "count", (B,))),
+                               B, n, H, D, page, _p(_opt_ints(status, "status", (B,))), _stream(stream)),
+           "spec_cache_append")
+
+
+def cache_read(pool, page_table, start, n: int, head_dim: int, count=None, *, k=None, v=None, status=None,
+               stream=None):
+    """Rows of the cache as bf16 values, exactly what the codes stand for:
+    (k, v), each [B, n, kv_heads, D]; rows i >= count[b] are 0."""
+    L = _lib()
+    page, H, pages = _pool(pool, 3, head_dim)
+    B, M = _table(page_table)
+    shape = (B, int(n), H, int(head_dim))
+    out = []
+    for t, name in ((k, "k"), (v, "v")):
+        if t is None:
+            t = torch.empty(shape, dtype=torch.bfloat16, device=pool.device)
+        elif _cuda(t, name, torch.bfloat16).shape != shape or not t.is_contiguous():
+            raise SpecError(f"{name} must be a contiguous {list(shape)} bf16 tensor")
+        out.append(t)
+    _check(L.spec_cache_read(_p(pool), pool.stride(0), pool.stride(1), pages,
+                             _p(page_table), page_table.stride(0), M,
+                             _p(_ints(start, "start", (B,))), _p(_opt_ints(count, "count", (B,))),
+                             B, int(n), H, int(head_dim), page, _p(out[0]), _p(out[1]),
+                             _p(_opt_ints(status, "status", (B,))), _stream(stream)), "spec_cache_read")
+    return out[0], out[1]
+
+
+@dataclass
+class CacheAttention:
+    out: torch.Tensor               # [B, n, q_heads, D] bf16
+    lse: Optional[torch.Tensor]     # [B, n, q_heads] fp32
+    ws: Optional[torch.Tensor]
+
+
+def cache_attend(q, pool, page_table, ctx_len, num_rows=None, *, anc_mask=None, depth=None, window: int = 0,
+                 sinks: int = 0, scale: Optional[float] = None, out=None, lse=None, want_lse: bool = False,
+                 status=None, ws: Optional[torch.Tensor] = None, stream=None) -> CacheAttention:
+    """Attention of drafted rows q [B, n, q_heads, D] bf16 over the cache.
+
+    Request b's cache holds ctx_len[b] context positions and behind them its
+    num_rows[b] (default n) drafted rows, written by cache_append.  A row sees
+    the context and, of the drafted rows, those in its anc_mask (int64
+    [B, n, ceil(n/64)], as tree_build writes it), or without a mask the rows up
+    to itself.  Its position is ctx_len[b] + depth[b, i] (default i); with
+    window > 0 it sees only keys of position p with p_i - p < window or
+    p < sinks.  scale defaults to 1/sqrt(D).  Rows that see nothing are 0, their
+    lse -inf; lse (natural log) is written when given or asked for."""
+    L = _lib()
+    _cuda(q, "q", torch.bfloat16)
+    if q.dim() != 4 or q.stride(3) != 1:
+        raise SpecError("q must be [B, n, q_heads, D] with unit element stride")
+    B, n, hq, D = q.shape
+    page, H, pages = _pool(pool, 3, D)
+    M = _table(page_table, B)[1]
+    dev = _dev(q)
+    if anc_mask is not None:
+        _cuda(anc_mask, "anc_mask", torch.int64)
+        if tuple(anc_mask.shape) != (B, n, (n + 63) // 64) or not anc_mask.is_contiguous():
+            raise SpecError("anc_mask must be a contiguous [B, n, ceil(n/64)] int64 tensor")
+    if out is None:
+        out = torch.empty((B, n, hq, D), dtype=torch.bfloat16, device=dev)
+    elif _cuda(out, "out", torch.bfloat16).shape != q.shape or not out.is_contiguous():
+        raise SpecError("out must be a contiguous tensor of q's shape, bf16")
+    if lse is None and want_lse:
+        lse = torch.empty((B, n, hq), dtype=torch.float32, device=dev)
+    elif lse is not None and (_cuda(lse, "lse", torch.float32).shape != (B, n, hq) or not lse.is_contiguous()):
+        raise SpecError("lse must be a contiguous [B, n, q_heads] float32 tensor")
+    need = L.spec_cache_attend_workspace_size(B, n, hq, H, D)
+    if ws is None and need > 0:
+        ws = workspace(need, dev)
+    _check(L.spec_cache_attend(_p(q), q.stride(0), q.stride(1), q.stride(2),
+                               _p(pool), pool.stride(0), pool.stride(1), pages,
+                               _p(page_table), page_table.stride(0), M,
+                               _p(_ints(ctx_len, "ctx_len", (B,))), _p(_opt_ints(num_rows, "num_rows", (B,))),
+                               _p(anc_mask), _p(_opt_ints(depth, "depth", (B, n))), int(window), int(sinks),
+                               1.0 / math.sqrt(D) if scale is None else float(scale),
+                               B, n, hq, H, D, page, _p(out), _p(lse), _p(_opt_ints(status, "status", (B,))),
+                               _p(ws), 0 if ws is None else ws.numel(), _stream(stream)), "spec_cache_attend")
+    return CacheAttention(out, lse, ws)
+
+
+def cache_compact(pool, page_table, ctx_len, path_nodes, num_accepted, head_dim: int, *, status=None,
+                  stream=None) -> None:
+    """Keep an accepted path's rows: position ctx_len[b] + path_nodes[b, j]
+    moves to ctx_len[b] + j, j = 0..num_accepted[b], in every layer of pool
+    [layers, pages, kv_heads, block].  In place."""
+    L = _lib()
+    page, H, pages = _pool(pool, 4, head_dim)
+    B, M = _table(page_table)
+    _cuda(path_nodes, "path_nodes", torch.int32)
+    if path_nodes.dim() != 2 or path_nodes.shape[0] != B or not path_nodes.is_contiguous():
+        raise SpecError("path_nodes must be a contiguous [B, path_width] int32 tensor")
+    _check(L.spec_cache_compact(_p(pool), pool.shape[0], pool.stride(0), pool.stride(1), pool.stride(2), pages,
+                                _p(page_table), page_table.stride(0), M, _p(_ints(ctx_len, "ctx_len", (B,))),
+                                _p(path_nodes), path_nodes.shape[1],
+                                _p(_ints(num_accepted, "num_accepted", (B,))),
+                                B, H, int(head_dim), page, _p(_opt_ints(status, "status", (B,))), _stream(stream)),
+           "spec_cache_compact")
+
+
+# ---------------------------------------------------------------------------
+# pages
+# ---------------------------------------------------------------------------
+@dataclass
+class PageState:
+    """Which request holds which page of a pool (int32 CUDA tensors)."""
+    page_table: torch.Tensor   # [R, M], -1 past num_held
+    num_held: torch.Tensor     # [R]
+    ref: torch.Tensor          # [num_pages]: requests that hold the page
+    free_list: torch.Tensor    # [num_pages]: a stack
+    num_free: torch.Tensor     # [1]
+
+
+def page_state(requests: int, max_pages: int, num_pages: int, device) -> PageState:
+    """A state in which every page is free; the stack's top is page 0."""
+    i32 = dict(dtype=torch.int32, device=device)
+    return PageState(torch.full((requests, max_pages), -1, **i32), torch.zeros(requests, **i32),
+                     torch.zeros(num_pages, **i32), torch.arange(num_pages - 1, -1, -1, **i32),
+                     torch.full((1,), num_pages, **i32))
+
+
+def _pages(s: PageState):
+    R, M = _table(s.page_table)
+    n = s.ref.shape[0]
+    _ints(s.num_held, "num_held", (R,))
+    _ints(s.ref, "ref", (n,))
+    _ints(s.free_list, "free_list", (n,))
+    _ints(s.num_free, "num_free", (1,))
+    return R, (_p(s.page_table), s.page_table.stride(0), M, _p(s.num_held), _p(s.ref), _p(s.free_list),
+               _p(s.num_free), n)
+
+
+def cache_reserve(pages: PageState, length, page_size: int, *, status=None, stream=None) -> None:
+    """Give each request the pages it lacks for length[r] tokens, off the top
+    of the stack, requests in order; one that they do not suffice for gets none
+    (ST_NO_PAGE)."""
+    R, args = _pages(pages)
+    _check(_lib().spec_cache_reserve(*args, _p(_ints(length, "length", (R,))), R, int(page_size),
+                                     _p(_opt_ints(status, "status", (R,))), _stream(stream)), "spec_cache_reserve")
+
+
+def cache_release(pages: PageState, length, page_size: int, *, status=None, stream=None) -> None:
+    """Each request keeps the pages of length[r] tokens (0: none); pages that
+    nothing holds any more are free."""
+    R, args = _pages(pages)
+    _check(_lib().spec_cache_release(*args, _p(_ints(length, "length", (R,))), R, int(page_size),
+                                     _p(_opt_ints(status, "status", (R,))), _stream(stream)), "spec_cache_release")
+
+
+def cache_fork(pool, pages: PageState, src, dst, length, head_dim: int, *, new_page=None, status=None, stream=None):
+    """Request dst[f] (holding nothing) becomes a copy of request src[f] at
+    length[src[f]] tokens: full pages are shared, the last partial one is copied
+    in every layer of pool [layers, pages, kv_heads, block].  Returns new_page
+    [F]: the page of its own that each got, or -1."""
+    L = _lib()
+    page, H, count = _pool(pool, 4, head_dim)
+    R, args = _pages(pages)
+    if pages.ref.shape[0] != count:
+        raise SpecError(f"the state has {pages.ref.shape[0]} pages, the pool {count}")
+    F = src.shape[0]
+    if new_page is None:
+        new_page = torch.empty(F, dtype=torch.int32, device=pool.device)
+    _check(L.spec_cache_fork(_p(pool), pool.shape[0], pool.stride(0), pool.stride(1), pool.stride(2), *args,
+                             _p(_ints(src, "src", (F,))), _p(_ints(dst, "dst", (F,))),
+                             _p(_ints(length, "length", (R,))), R, F, H, int(head_dim), page,
+                             _p(_ints(new_page, "new_page", (F,))), _p(_opt_ints(status, "status", (F,))),
+                             _stream(stream)), "spec_cache_fork")
+    return new_page

@@ -11,8 +11,9 @@
 
 #include "../../include/spec_verify.h"
 #include "spec_chain.cuh"
+#include "spec_host.cuh"
 
-namespace {
+namespace spec {
 
 thread_local std::string g_err;
 
@@ -30,6 +31,14 @@ spec_status cuda_fail(cudaError_t e, const char* where) {
     return fail(SPEC_CUDA_ERROR, "%s: %s", where, cudaGetErrorString(e));
 }
 
+}  // namespace spec
+
+namespace {
+
+using spec::cuda_fail;
+using spec::fail;
+using spec::g_err;
+
 int g_tune_c = 0;        // CTAs per cluster (0 = automatic)
 int g_tune_spc = 0;      // slots per CTA (0 = automatic)
 
@@ -42,48 +51,6 @@ size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool valid_dtype(spec_dtype d) { return d == SPEC_F32 || d == SPEC_BF16; }
 int esize_of(spec_dtype d) { return d == SPEC_F32 ? 4 : 2; }
-
-// Where an array lives.  Device (and managed) memory is used as it is;
-// pinned host memory is read and written in place through its mapping into
-// the device's address space (on a Grace host, over the NVLink-C2C link);
-// pageable host memory cannot be reached by the kernels and is refused.
-template <class T>
-spec_status map_ptr(const char* who, const char* name, T*& p) {
-    if (!p) return SPEC_OK;
-    cudaPointerAttributes a;
-    if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
-        cudaGetLastError();
-        return fail(SPEC_INVALID_ARG, "%s: %s is not memory the device can reach", who, name);
-    }
-    if (a.type == cudaMemoryTypeDevice || a.type == cudaMemoryTypeManaged) return SPEC_OK;
-    if (a.type == cudaMemoryTypeHost && a.devicePointer) {
-        p = static_cast<T*>(a.devicePointer);
-        return SPEC_OK;
-    }
-    return fail(SPEC_INVALID_ARG, "%s: %s is pageable host memory (pass device memory or pinned host memory)", who,
-                name);
-}
-#define SPEC_MAP(x)                                              \
-    do {                                                         \
-        const spec_status map_s_ = map_ptr(who, #x, x);          \
-        if (map_s_ != SPEC_OK) return map_s_;                    \
-    } while (0)
-
-// The workspace holds the kernels' queues, flags and partial results: it must
-// be device memory.
-spec_status ws_on_device(const char* who, const void* ws) {
-    cudaPointerAttributes a;
-    if (cudaPointerGetAttributes(&a, ws) != cudaSuccess || a.type != cudaMemoryTypeDevice) {
-        cudaGetLastError();
-        return fail(SPEC_INVALID_ARG, "%s: the workspace must be device memory", who);
-    }
-    return SPEC_OK;
-}
-#define SPEC_WS_DEVICE(w)                                        \
-    do {                                                         \
-        const spec_status ws_s_ = ws_on_device(who, w);          \
-        if (ws_s_ != SPEC_OK) return ws_s_;                      \
-    } while (0)
 
 // Bulk copies (TMA) need device memory: host memory mapped into the device's
 // address space is read with plain loads.
