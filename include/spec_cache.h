@@ -43,6 +43,9 @@ extern "C" {
 #define SPEC_ST_BAD_PAGE 128   /* a needed position has no page (or a page id / request id out of range) */
 #define SPEC_ST_NO_PAGE  256   /* the free pages did not suffice: the request got none */
 
+/* bytes at the start of spec_cache_attend's workspace that begin zeroed */
+#define SPEC_CACHE_WS_CONTROL 16384
+
 /* bytes of one block (one page of one kv head); 0 if the shape is not supported */
 size_t spec_cache_block_bytes(int head_dim, int page_size);
 
@@ -94,7 +97,8 @@ spec_status spec_cache_read(
  *   num_rows NULL (n each) or [B] (cut to [0, n]); ctx_len is cut to what the
  *            table can hold.
  *   anc_mask NULL or [B, n, ceil(n/64)] uint64, as spec_tree_build writes it;
- *            depth NULL or [B, n] int32 (both, or a mask alone: depth = i).
+ *            depth NULL or [B, n] int32, cut to [0, n] (both, or a mask
+ *            alone: depth = i).
  *   scale    multiplies q . k (> 0, finite).
  * Outputs: out bf16 [B, n, q_heads, D] contiguous: softmax over the seen keys
  *   times V; lse NULL or fp32 [B, n, q_heads]: natural log of the softmax's
@@ -102,6 +106,11 @@ spec_status spec_cache_read(
  *   lse = -inf.  Keys that no row sees contribute nothing whatever the cache
  *   holds there.  Scales of seen positions must be finite, as
  *   spec_cache_append writes them.
+ *   ws       sized by the query for the same shape, 16-byte aligned; its first
+ *            SPEC_CACHE_WS_CONTROL bytes must be zero before the first call
+ *            and are zero again after every call (except the error word that
+ *            spec_workspace_error reads).  One workspace serves calls of any
+ *            shape that fits it, one after another.
  * 1 <= n <= 1024.  Deterministic: the same inputs give the same bits.
  * ---------------------------------------------------------------------- */
 size_t spec_cache_attend_workspace_size(int B, int n, int q_heads, int kv_heads, int head_dim);

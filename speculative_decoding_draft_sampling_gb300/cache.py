@@ -28,7 +28,7 @@ from typing import Optional
 
 import torch
 
-from . import SpecError, _check, _cuda, _dev, _load, _p, _stream, workspace
+from . import SpecError, _check, _cuda, _dev, _load, _p, _stream
 
 ST_BAD_PAGE, ST_NO_PAGE = 128, 256
 
@@ -154,6 +154,25 @@ class CacheAttention:
     ws: Optional[torch.Tensor]
 
 
+_attend_ws: dict = {}
+
+
+def _attend_workspace(nbytes: int, device: torch.device, stream) -> torch.Tensor:
+    """cache_attend's workspace, one per device and stream: its control words
+    start at zero and every call leaves them so."""
+    handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    key = (device.index, handle)
+    buf = _attend_ws.get(key)
+    if buf is None or buf.numel() < nbytes:
+        if torch.cuda.is_current_stream_capturing():
+            raise SpecError("cache_attend needs its workspace before a stream capture: call it once before, or pass ws "
+                            "(zeroed)")
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device)):
+            buf = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+        _attend_ws[key] = buf
+    return buf
+
+
 def cache_attend(q, pool, page_table, ctx_len, num_rows=None, *, anc_mask=None, depth=None, window: int = 0,
                  sinks: int = 0, scale: Optional[float] = None, out=None, lse=None, want_lse: bool = False,
                  status=None, ws: Optional[torch.Tensor] = None, stream=None) -> CacheAttention:
@@ -166,7 +185,8 @@ def cache_attend(q, pool, page_table, ctx_len, num_rows=None, *, anc_mask=None, 
     to itself.  Its position is ctx_len[b] + depth[b, i] (default i); with
     window > 0 it sees only keys of position p with p_i - p < window or
     p < sinks.  scale defaults to 1/sqrt(D).  Rows that see nothing are 0, their
-    lse -inf; lse (natural log) is written when given or asked for."""
+    lse -inf; lse (natural log) is written when given or asked for.  A ws of
+    one's own starts zeroed and serves one stream."""
     L = _lib()
     _cuda(q, "q", torch.bfloat16)
     if q.dim() != 4 or q.stride(3) != 1:
@@ -189,7 +209,7 @@ def cache_attend(q, pool, page_table, ctx_len, num_rows=None, *, anc_mask=None, 
         raise SpecError("lse must be a contiguous [B, n, q_heads] float32 tensor")
     need = L.spec_cache_attend_workspace_size(B, n, hq, H, D)
     if ws is None and need > 0:
-        ws = workspace(need, dev)
+        ws = _attend_workspace(need, dev, stream)
     _check(L.spec_cache_attend(_p(q), q.stride(0), q.stride(1), q.stride(2),
                                _p(pool), pool.stride(0), pool.stride(1), pages,
                                _p(page_table), page_table.stride(0), M,

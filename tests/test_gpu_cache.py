@@ -386,10 +386,10 @@ def test_attend_same_bits_every_time_and_on_another_stream():
     c = ints(ctx)
     torch.cuda.synchronize()
     side = torch.cuda.Stream()
-    ws = None if first.ws is None else torch.empty_like(first.ws)
+    ws = None if first.ws is None else torch.zeros_like(first.ws)
     with torch.cuda.stream(side):
         other = sv.cache_attend(q, pool, table, c, want_lse=True, ws=ws)
-    given = sv.cache_attend(q, pool, table, c, want_lse=True, ws=None if ws is None else torch.empty_like(ws), stream=side)
+    given = sv.cache_attend(q, pool, table, c, want_lse=True, ws=None if ws is None else torch.zeros_like(ws), stream=side)
     side.synchronize()
     assert torch.equal(first.out, other.out) and torch.equal(first.out, given.out)
 
@@ -400,7 +400,7 @@ def test_attend_in_a_graph():
     q, c = randn(2, 4, 8, D), ints([1996, 296])
     want = sv.cache_attend(q, pool, table, c, want_lse=True)
     out, lse = torch.zeros_like(want.out), torch.zeros_like(want.lse)
-    ws = None if want.ws is None else torch.empty_like(want.ws)
+    ws = None if want.ws is None else torch.zeros_like(want.ws)
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
         sv.cache_attend(q, pool, table, c, out=out, lse=lse, ws=ws)
