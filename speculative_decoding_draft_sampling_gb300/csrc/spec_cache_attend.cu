@@ -215,7 +215,7 @@ struct AttendCfg {
     static constexpr int kStageBytes = kTile * CacheBlock<D>::kTok;
     static constexpr int kCtas = 3;                         // resident CTAs an SM
     static constexpr int kStages = D == 128 ? 2 : 4;
-    static constexpr int kMB = NT == 1 ? 4 : 2;             // 16-token blocks whose scores are held at once
+    static constexpr int kMB = 2;                           // 16-token blocks whose scores are held at once
     static constexpr int kRows = 8 * NT;
     static constexpr int kPad = D + 4;                      // pitch of a row when warps are joined
     static constexpr int kRing = kAtWarps * kStages * kStageBytes;
@@ -223,7 +223,7 @@ struct AttendCfg {
     static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
 };
 
-template <int D, int NT>
+template <int D, int NT, int P>
 __global__ void __launch_bounds__(kAtThreads, AttendCfg<D, NT>::kCtas)
 cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_constant__ AttendPlan L) {
     using Cfg = AttendCfg<D, NT>;
@@ -238,12 +238,14 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
     __shared__ long long s_found[2];
     __shared__ int s_last;
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);    // uniform to the compiler too
     const int r8 = lane >> 2, c4 = lane & 3;
     const int H = A.pool.heads;
-    const int P = A.pool.P, p_shift = A.pool.p_shift;
-    const int ppt = kTile >> p_shift;           // page blocks a tile
-    const int block_bytes = Blk::bytes(P);
+    constexpr int p_shift = P == 64 ? 6 : P == 32 ? 5 : 4;
+    constexpr int ppt = kTile / P;              // page blocks a tile
+    constexpr int per = 32 / ppt;               // tiles whose page ids a warp holds
+    constexpr int block_bytes = Blk::bytes(P);
 
     if (lane == 0) {
 #pragma unroll
@@ -319,6 +321,12 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
     const int tok = r8 ^ ((r8 >> 1) & 1);       // the token (of 8) that is row r8 of S^T
     const int tv0 = (2 * c4) ^ (c4 & 1);        // tokens 2c and 2c+1 of P^T's rows
     const int tv1 = (2 * c4 + 1) ^ (c4 & 1);
+    // where a lane's words and scales lie from the start of a block's 16 tokens
+    const uint32_t k_at = tok * Blk::kRow + c4 * (D / 8);
+    const uint32_t ks_at = P * Blk::kRow + tok * Blk::kScl + (D == 128 ? c4 : c4 >> 1) * 2;
+    const uint32_t v_at = Blk::v_codes(P) + r8 * (D / 16), vs_at = Blk::v_codes(P) + P * Blk::kRow + (D == 128 ? r8 >> 1 : r8 >> 2) * 2;
+    const uint32_t v0_at = v_at + tv0 * Blk::kRow, v1_at = v_at + tv1 * Blk::kRow;
+    const uint32_t vs0_at = vs_at + tv0 * Blk::kScl, vs1_at = vs_at + tv1 * Blk::kScl;
 
     for (long long pos = lo; pos < hi;) {
         // ---- the unit that holds tile pos -----------------------------------
@@ -350,7 +358,6 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
         const int live_rows = min(max(rq.rows * A.G - row0, 0), kRows);
 
         // ---- page ids: a lane per page block of the coming tiles ------------
-        const int per = 32 / ppt;               // tiles whose ids a warp holds
         int entry = -2;
         auto load_entries = [&](int k0) {
             const int v = v0 + warp + kAtWarps * (k0 + lane / ppt);
@@ -464,13 +471,12 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
                 for (int mb = 0; mb < kMB; ++mb) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) x[mb][nt][0] = x[mb][nt][1] = x[mb][nt][2] = x[mb][nt][3] = 0.0f;
-                    const int t = (g * kMB + mb) * 16;
+                    const int t = (g * kMB + mb) * 16, slot = t & (P - 1);
                     const uint32_t blk = stage + (t >> p_shift) * block_bytes;
-                    const int slot = (t & (P - 1)) + tok;
+                    const uint32_t kr = blk + slot * Blk::kRow + k_at, sc = blk + slot * Blk::kScl + ks_at;
                     uint32_t wa[kKW], wb[kKW];
-                    lds(wa, blk + slot * Blk::kRow + c4 * (D / 8));
-                    lds(wb, blk + (slot + 8) * Blk::kRow + c4 * (D / 8));
-                    const uint32_t sc = blk + P * Blk::kRow + slot * Blk::kScl + (D == 128 ? c4 : c4 >> 1) * 2;
+                    lds(wa, kr);
+                    lds(wb, kr + 8 * Blk::kRow);
                     const uint32_t sa = lds16(sc) * 0x10001u, sb = lds16(sc + 8 * Blk::kScl) * 0x10001u;
                     const uint32_t ca = minus1_5(sa), cb = minus1_5(sb);
 #pragma unroll
@@ -570,18 +576,16 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
                         mma(lr[nt], ones, pf[mb][nt][0], pf[mb][nt][1]);
                         if constexpr (kMasked) mma(lr[nt], ones, pl[mb][nt][0], pl[mb][nt][1]);
                     }
-                    const int t = (g * kMB + mb) * 16;
-                    const uint32_t blk = stage + (t >> p_shift) * block_bytes + Blk::v_codes(P);
-                    const int slot = t & (P - 1);
-                    const uint32_t vrow = blk + r8 * (D / 16);
-                    const uint32_t vscl = blk + P * Blk::kRow + (D == 128 ? r8 >> 1 : r8 >> 2) * 2;
+                    const int t = (g * kMB + mb) * 16, slot = t & (P - 1);
+                    const uint32_t blk = stage + (t >> p_shift) * block_bytes;
+                    const uint32_t vr = blk + slot * Blk::kRow, vs = blk + slot * Blk::kScl;
                     uint32_t w0[kVW], w1[kVW], w2[kVW], w3[kVW];
-                    lds(w0, vrow + (slot + tv0) * Blk::kRow);
-                    lds(w1, vrow + (slot + tv1) * Blk::kRow);
-                    lds(w2, vrow + (slot + tv0 + 8) * Blk::kRow);
-                    lds(w3, vrow + (slot + tv1 + 8) * Blk::kRow);
-                    uint32_t s0 = lds16(vscl + (slot + tv0) * Blk::kScl), s1 = lds16(vscl + (slot + tv1) * Blk::kScl);
-                    uint32_t s2 = lds16(vscl + (slot + tv0 + 8) * Blk::kScl), s3 = lds16(vscl + (slot + tv1 + 8) * Blk::kScl);
+                    lds(w0, vr + v0_at);
+                    lds(w1, vr + v1_at);
+                    lds(w2, vr + v0_at + 8 * Blk::kRow);
+                    lds(w3, vr + v1_at + 8 * Blk::kRow);
+                    uint32_t s0 = lds16(vs + vs0_at), s1 = lds16(vs + vs1_at);
+                    uint32_t s2 = lds16(vs + vs0_at + 8 * Blk::kScl), s3 = lds16(vs + vs1_at + 8 * Blk::kScl);
                     if constexpr (kMasked) {    // what no row sees may be anything, NaN among it
                         const uint32_t a = static_cast<uint32_t>(any >> t);
                         s0 = a >> tv0 & 1 ? s0 : 0;
@@ -666,50 +670,48 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
             parts = cta_of(u_from + nt_unit - 1) - c0 + 1;
         }
         const int slot = 2 * cta + (c0 == cta ? 1 : 0);
-        auto emit = [&](int row, int place, float v, float lsum) {
-            // place -> d
-            const int rr = place & 7, jj = place >> 3, half = jj >= kMT, j = jj - half * kMT;
-            const int d = rr * (D / 8) + (j >> 2) * 8 + (j & 3) + 4 * half;
-            const int rho = row0 + row, i = rho / A.G, g = rho % A.G;
-            const long long at = (static_cast<long long>(b) * A.n + i) * A.hq + static_cast<long long>(h) * A.G + g;
-            const float r = lsum == 0.0f ? 0.0f : 16.0f * v / lsum;
-            A.out[at * D + d] = __bfloat16_as_ushort(__float2bfloat16_rn(r));
-        };
-        auto emit_lse = [&](int row, float mm, float lsum) {
-            if (!A.lse) return;
-            const int rho = row0 + row, i = rho / A.G, g = rho % A.G;
-            const long long at = (static_cast<long long>(b) * A.n + i) * A.hq + static_cast<long long>(h) * A.G + g;
-            A.lse[at] = lsum == 0.0f ? -CUDART_INF_F : (mm + log2f(lsum)) * kLn2;
-        };
+        // An item is eight neighbouring values of a row: (row, r8, w).
+        constexpr int kItems = kRows * (D / 8);
         const int rows_here = min(kRows, A.n * A.G - row0);     // rows of the output in this block
-        for (int x = tid; x < kRows * D; x += kAtThreads) {
-            const int row = x / D, place = x % D;
+        auto emit = [&](int row, int item, const float (&v)[8], float mm, float ls, float lrs) {
+            const int rho = row0 + row, i = rho / A.G, g = rho % A.G;
+            const long long at = (static_cast<long long>(b) * A.n + i) * A.hq + static_cast<long long>(h) * A.G + g;
+            const bool on = row < live_rows && ls != 0.0f;
+            const float f = on ? 16.0f / lrs : 0.0f;
+            uint4 u;
+            u.x = on ? pack_bf16(v[0] * f, v[1] * f) : 0;
+            u.y = on ? pack_bf16(v[2] * f, v[3] * f) : 0;
+            u.z = on ? pack_bf16(v[4] * f, v[5] * f) : 0;
+            u.w = on ? pack_bf16(v[6] * f, v[7] * f) : 0;
+            *reinterpret_cast<uint4*>(A.out + at * D + item * 8) = u;
+            if (A.lse && item == 0) A.lse[at] = on ? (mm + log2f(ls)) * kLn2 : -CUDART_INF_F;
+        };
+#pragma unroll
+        for (int x = tid; x < kItems; x += kAtThreads) {
+            const int row = x / (D / 8), item = x % (D / 8);    // values 8 item .. 8 item + 7 of the row
+            const int rr = item / kVW, w8 = item % kVW;
             float mm = kNoMax;
 #pragma unroll
             for (int w = 0; w < kAtWarps; ++w) mm = fmaxf(mm, jm[(w * kRows + row) * 3]);
-            float v = 0.0f, ls = 0.0f, lrs = 0.0f;
+            float v[8] = {}, ls = 0.0f, lrs = 0.0f;
 #pragma unroll
             for (int w = 0; w < kAtWarps; ++w) {
                 const float* ml = jm + (w * kRows + row) * 3;
                 const float f = exp2_fast(ml[0] - mm);
-                v += f * jo[(w * kRows + row) * kPad + place];
                 ls += f * ml[1];
                 lrs += f * ml[2];
+                const float* src = jo + (w * kRows + row) * kPad + w8 * 32 + rr;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] += f * src[(e >= 4 ? kMT * 8 : 0) + (e & 3) * 8];
             }
             if (whole) {
-                if (row < rows_here) {
-                    const bool on = row < live_rows;
-                    emit(row, place, v, on ? lrs : 0.0f);
-                    if (place == 0) emit_lse(row, mm, on ? ls : 0.0f);
-                }
+                if (row < rows_here) emit(row, item, v, mm, ls, lrs);
             } else {
-                L.part[(static_cast<long long>(slot) * kRows + row) * D + place] = v;
-                if (place == 0) {
-                    float* ml = L.ml + (slot * kRows + row) * 4;
-                    ml[0] = mm;
-                    ml[1] = ls;
-                    ml[2] = lrs;
-                }
+                float4* to = reinterpret_cast<float4*>(L.part + (static_cast<long long>(slot) * kRows + row) * D + item * 8);
+                __stcg(to, make_float4(v[0], v[1], v[2], v[3]));
+                __stcg(to + 1, make_float4(v[4], v[5], v[6], v[7]));
+                if (item == 0)
+                    __stcg(reinterpret_cast<float4*>(L.ml) + slot * kRows + row, make_float4(mm, ls, lrs, 0.0f));
             }
         }
         if (!whole) {
@@ -723,23 +725,25 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
             __syncthreads();
             if (s_last) {
                 __threadfence();
-                for (int x = tid; x < rows_here * D; x += kAtThreads) {
-                    const int row = x / D, place = x % D;
-                    float mm = kNoMax, v = 0.0f, ls = 0.0f, lrs = 0.0f;
+                for (int x = tid; x < rows_here * (D / 8); x += kAtThreads) {
+                    const int row = x / (D / 8), item = x % (D / 8);
+                    auto place = [&](int c) { return (2ll * (c0 + c) + (c == 0 ? 1 : 0)) * kRows + row; };
+                    float mm = kNoMax;
+#pragma unroll 4
+                    for (int c = 0; c < parts; ++c) mm = fmaxf(mm, __ldcg(L.ml + place(c) * 4));
+                    float v[8] = {}, ls = 0.0f, lrs = 0.0f;
+#pragma unroll 4
                     for (int c = 0; c < parts; ++c) {
-                        const long long sl = (2ll * (c0 + c) + (c == 0 ? 1 : 0)) * kRows + row;
-                        const float4 ml = __ldcg(reinterpret_cast<const float4*>(L.ml) + sl);
-                        const float vc = __ldcg(L.part + sl * D + place);
-                        const float mn = fmaxf(mm, ml.x);
-                        const float f = exp2_fast(mm - mn), fc = exp2_fast(ml.x - mn);
-                        mm = mn;
-                        v = v * f + vc * fc;
-                        ls = ls * f + ml.y * fc;
-                        lrs = lrs * f + ml.z * fc;
+                        const float4 ml = __ldcg(reinterpret_cast<const float4*>(L.ml) + place(c));
+                        const float4* from = reinterpret_cast<const float4*>(L.part + place(c) * D + item * 8);
+                        const float4 a = __ldcg(from), z = __ldcg(from + 1);
+                        const float f = exp2_fast(ml.x - mm);
+                        ls += f * ml.y;
+                        lrs += f * ml.z;
+                        v[0] += f * a.x; v[1] += f * a.y; v[2] += f * a.z; v[3] += f * a.w;
+                        v[4] += f * z.x; v[5] += f * z.y; v[6] += f * z.z; v[7] += f * z.w;
                     }
-                    const bool on = row < live_rows;
-                    emit(row, place, v, on ? lrs : 0.0f);
-                    if (place == 0) emit_lse(row, mm, on ? ls : 0.0f);
+                    emit(row, item, v, mm, ls, lrs);
                 }
             }
         }
@@ -775,7 +779,7 @@ Layout layout_of(int grid, int NT, int D) {
     return y;
 }
 
-template <int D, int NT>
+template <int D, int NT, int P>
 cudaError_t attend(const CacheAttendArgs& A, cudaStream_t st) {
     using Cfg = AttendCfg<D, NT>;
     const int grid = min(sm_count() * Cfg::kCtas, kMaxGrid);
@@ -788,10 +792,10 @@ cudaError_t attend(const CacheAttendArgs& A, cudaStream_t st) {
     L.ctrl = reinterpret_cast<AttendCtrl*>(ws);
     L.ml = reinterpret_cast<float*>(ws + y.ml);
     L.part = reinterpret_cast<float*>(ws + y.part);
-    const cudaError_t e = cudaFuncSetAttribute(cache_attend_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(cache_attend_kernel<D, NT, P>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                Cfg::kSmem);
     if (e != cudaSuccess) return e;
-    cache_attend_kernel<D, NT><<<grid, kAtThreads, Cfg::kSmem, st>>>(A, L);
+    cache_attend_kernel<D, NT, P><<<grid, kAtThreads, Cfg::kSmem, st>>>(A, L);
     return cudaGetLastError();
 }
 
@@ -803,10 +807,23 @@ size_t cache_attend_ws(int B, int n, int hq, int hkv, int D) {
     return layout_of(min(sm_count() * 3, kMaxGrid), NT, D).bytes;
 }
 
+namespace {
+
+template <int D, int NT>
+cudaError_t attend_pages(const CacheAttendArgs& A, cudaStream_t st) {
+    switch (A.pool.P) {
+        case 16: return attend<D, NT, 16>(A, st);
+        case 32: return attend<D, NT, 32>(A, st);
+        default: return attend<D, NT, 64>(A, st);
+    }
+}
+
+}  // namespace
+
 cudaError_t cache_attend_run(const CacheAttendArgs& A, cudaStream_t st) {
     const int NT = row_blocks(A.n * A.G);
-    if (A.pool.D == 128) return NT == 1 ? attend<128, 1>(A, st) : attend<128, 2>(A, st);
-    return NT == 1 ? attend<64, 1>(A, st) : attend<64, 2>(A, st);
+    if (A.pool.D == 128) return NT == 1 ? attend_pages<128, 1>(A, st) : attend_pages<128, 2>(A, st);
+    return NT == 1 ? attend_pages<64, 1>(A, st) : attend_pages<64, 2>(A, st);
 }
 
 }  // namespace spec
