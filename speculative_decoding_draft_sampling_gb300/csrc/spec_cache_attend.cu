@@ -18,14 +18,15 @@
 // requests' lengths; a unit that several CTAs share is joined by the last of
 // them to finish, in CTA order (so the bits do not depend on timing).
 //
-// A warp takes every fourth tile of its CTA's share and is a pipeline of its
-// own: one bulk copy (TMA) per page block into its ring in shared memory, no
-// barrier with other warps.  Codes go from there straight into the registers
-// of the tensor instruction (mma m16n8k16): scores are computed transposed,
-// S^T = K Q^T and O^T = V^T P^T, so that the cache's side is the 16-row operand
-// and the few rows of a request fill 8-column blocks instead of padding a
-// 16-row tile.  A lane's 32 (D = 128) values of a key are 16 consecutive bytes
-// of its row: the order of the k index is free as long as Q is laid out alike.
+// A tile.  Bulk copies (TMA), one per page block, bring a tile into a ring in
+// shared memory.  Codes go from there straight into the registers of the tensor
+// instruction (mma m16n8k16): scores are computed transposed, S^T = K Q^T and
+// O^T = V^T P^T, so that the cache's side is the 16-row operand and the few
+// rows of a request fill 8-column blocks instead of padding a 16-row tile.
+// Four warps share a tile: each takes 16 tokens of S^T and then, P^T having
+// gone through shared memory, a quarter of the D rows of O^T over all 64
+// tokens.  No code is decoded twice, a warp's share of O^T is small enough for
+// many CTAs an SM, and one barrier a tile is all they wait for each other.
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
@@ -142,6 +143,20 @@ __device__ __forceinline__ void lds(uint32_t (&w)[kWords], uint32_t a) {
     else
         asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(a));
 }
+// a lane's codes of a value row: D/32 of them
+template <int D>
+__device__ __forceinline__ uint32_t ldsv(uint32_t a) {
+    if constexpr (D == 128) {
+        return lds16(a);
+    } else {
+        uint32_t v;
+        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+        return v;
+    }
+}
+__device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
+    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" :: "r"(a), "r"(x), "r"(y) : "memory");
+}
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -210,67 +225,74 @@ __device__ __forceinline__ unsigned long long seen64(const CacheAttendArgs& A, c
 // ---------------------------------------------------------------------------
 // the kernel
 // ---------------------------------------------------------------------------
+constexpr int ctas_of(int NT) { return NT == 1 ? 6 : NT <= 3 ? 5 : NT == 4 ? 4 : NT <= 6 ? 3 : 2; }
+
 template <int D, int NT>
 struct AttendCfg {
-    static constexpr int kStageBytes = kTile * CacheBlock<D>::kTok;
-    static constexpr int kCtas = 3;                         // resident CTAs an SM
-    static constexpr int kStages = D == 128 ? 2 : 4;
-    static constexpr int kMB = 2;                           // 16-token blocks whose scores are held at once
     static constexpr int kRows = 8 * NT;
-    static constexpr int kPad = D + 4;                      // pitch of a row when warps are joined
-    static constexpr int kRing = kAtWarps * kStages * kStageBytes;
-    static constexpr int kJoin = kAtWarps * kRows * (kPad + 3) * 4;
-    static constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
+    static constexpr int kStages = D == 128 ? 3 : 4;
+    static constexpr int kStageBytes = kTile * CacheBlock<D>::kTok;
+    static constexpr int kP = 4 * NT * 256;                 // P^T of a tile: [16 tokens][NT][lane] of 8 bytes
+    static constexpr int kQ = (D / 16) * NT * 256;          // Q: [k step][NT][lane] of 8 bytes
+    static constexpr int kSmem = kStages * kStageBytes + kQ + 3 * kP;
+    // resident CTAs an SM: what registers (O^T, S^T) and shared memory allow
+    static constexpr int kCtas = ctas_of(NT);
+    static constexpr bool kQInRegs = NT == 1;
 };
 
-template <int D, int NT, int P>
+template <int D, int NT>
 __global__ void __launch_bounds__(kAtThreads, AttendCfg<D, NT>::kCtas)
 cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_constant__ AttendPlan L) {
     using Cfg = AttendCfg<D, NT>;
     using Blk = CacheBlock<D>;
-    constexpr int kS = Cfg::kStages, kMB = Cfg::kMB, kRows = Cfg::kRows, kPad = Cfg::kPad;
+    constexpr int kS = Cfg::kStages, kRows = Cfg::kRows;
     constexpr int kKW = D / 32;                 // words of a key that a lane holds
-    constexpr int kVW = D / 64;                 // words of a value row that a lane holds
-    constexpr int kMT = D / 16;                 // 16-row blocks of O^T
+    constexpr int kMT = D / 64;                 // 16-row blocks of O^T that a warp holds
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ uint64_t full[kAtWarps][kS];
+    __shared__ uint64_t full[kS];
     __shared__ long long s_sum[kAtWarps];
     __shared__ long long s_found[2];
-    __shared__ int s_last;
+    __shared__ long long s_q[kRows], s_out[kRows];          // a row's place in q and in out / lse (-1: none)
+    __shared__ unsigned long long s_seen[kRows];
+    __shared__ float s_max[kAtWarps][kRows];
+    __shared__ float s_l[kAtWarps][kRows], s_lr[kRows];
+    __shared__ int s_last, s_dead;
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);    // uniform to the compiler too
     const int r8 = lane >> 2, c4 = lane & 3;
     const int H = A.pool.heads;
-    constexpr int p_shift = P == 64 ? 6 : P == 32 ? 5 : 4;
-    constexpr int ppt = kTile / P;              // page blocks a tile
-    constexpr int per = 32 / ppt;               // tiles whose page ids a warp holds
-    constexpr int block_bytes = Blk::bytes(P);
+    const int P = A.pool.P, p_shift = A.pool.p_shift;
+    const int ppt_shift = 6 - p_shift, ppt = 1 << ppt_shift;    // page blocks a tile
+    const int block_bytes = Blk::bytes(P);
+    const uint32_t ring = smem_u32(smem);
+    const uint32_t q_base = ring + kS * Cfg::kStageBytes, p_base = q_base + Cfg::kQ, lo_base = p_base + 2 * Cfg::kP;
 
-    if (lane == 0) {
+    if (tid == 0) {
 #pragma unroll
-        for (int s = 0; s < kS; ++s) mbar_init(&full[warp][s], 1);
+        for (int s = 0; s < kS; ++s) mbar_init(&full[s], 1);
         fence_mbar_init();
+        s_dead = 0;
     }
 
     // ---- this CTA's share: [lo, hi) of all tiles ---------------------------
-    auto block_sum = [&](long long v) {
-#pragma unroll
-        for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == 0) s_sum[warp] = v;
-        __syncthreads();
-        v = 0;
-#pragma unroll
-        for (int w = 0; w < kAtWarps; ++w) v += s_sum[w];
-        __syncthreads();
-        return v;
-    };
     auto work_of = [&](int b) {
         return b < A.B ? static_cast<long long>(H) * head_work(A, request(A, b), L.row_tiles, kRows) : 0ll;
     };
-    long long mine = 0;
-    for (int b = tid; b < A.B; b += kAtThreads) mine += work_of(b);
-    const long long total = block_sum(mine);
+    // the requests a chunk of threads at a time; one chunk is the usual case
+    long long total = 0, first_work = 0;
+    for (int b0 = 0; b0 < A.B; b0 += kAtThreads) {
+        const long long v = work_of(b0 + tid);
+        if (b0 == 0) first_work = v;
+        total += v;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    if (lane == 0) s_sum[warp] = total;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kAtWarps; ++w) total += s_sum[w];
     const long long units = static_cast<long long>(A.B) * H * L.row_tiles;
     long long want = total / L.min_tiles;
     if (want > units * 64) want = units * 64;   // what joins a unit must stay small beside it
@@ -279,11 +301,12 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
     if (cta >= active) return;
     auto start_of = [&](long long c) { return c * total / active; };
     const long long lo = start_of(cta), hi = start_of(cta + 1);
+    __syncthreads();
     // the request that holds tile lo, and where its tiles start
     {
         long long before = 0;
         for (int b0 = 0; b0 < A.B; b0 += kAtThreads) {
-            const long long v = work_of(b0 + tid);
+            const long long v = b0 == 0 ? first_work : work_of(b0 + tid);
             long long inc = v;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -312,183 +335,203 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
     long long b_from = s_found[1];
     Req rq = request(A, b);
 
-    bool dead = false;                          // a wait gave up: nothing more is copied or waited for
-    uint32_t phase[kS];
-#pragma unroll
-    for (int s = 0; s < kS; ++s) phase[s] = 0;
-    unsigned char* ring = smem + warp * kS * Cfg::kStageBytes;
-    const uint32_t ring_u32 = smem_u32(ring);
+    uint32_t phases = 0;                        // one bit a stage
     const int tok = r8 ^ ((r8 >> 1) & 1);       // the token (of 8) that is row r8 of S^T
     const int tv0 = (2 * c4) ^ (c4 & 1);        // tokens 2c and 2c+1 of P^T's rows
     const int tv1 = (2 * c4 + 1) ^ (c4 & 1);
-    // where a lane's words and scales lie from the start of a block's 16 tokens
-    const uint32_t k_at = tok * Blk::kRow + c4 * (D / 8);
-    const uint32_t ks_at = P * Blk::kRow + tok * Blk::kScl + (D == 128 ? c4 : c4 >> 1) * 2;
-    const uint32_t v_at = Blk::v_codes(P) + r8 * (D / 16), vs_at = Blk::v_codes(P) + P * Blk::kRow + (D == 128 ? r8 >> 1 : r8 >> 2) * 2;
+    // where a lane's words and scales lie in a tile: its key (this warp's 16
+    // tokens), and from the start of 16 tokens its part of the values
+    auto at16 = [&](int mb, int row_bytes) {    // rows of the mb-th 16 tokens
+        return ((mb * 16) >> p_shift) * block_bytes + ((mb * 16) & (P - 1)) * row_bytes;
+    };
+    const uint32_t k_at = at16(warp, Blk::kRow) + tok * Blk::kRow + c4 * (D / 8);
+    const uint32_t ks_at = at16(warp, Blk::kScl) + P * Blk::kRow + tok * Blk::kScl + (D == 128 ? c4 : c4 >> 1) * 2;
+    const uint32_t v_at = Blk::v_codes(P) + warp * (D / 8) + r8 * (D / 64);
+    const uint32_t vs_at = Blk::v_codes(P) + P * Blk::kRow + (D == 128 ? warp : warp >> 1) * 2;
     const uint32_t v0_at = v_at + tv0 * Blk::kRow, v1_at = v_at + tv1 * Blk::kRow;
     const uint32_t vs0_at = vs_at + tv0 * Blk::kScl, vs1_at = vs_at + tv1 * Blk::kScl;
+    const float cs = A.scale * kLog2e * 16.0f;
 
     for (long long pos = lo; pos < hi;) {
         // ---- the unit that holds tile pos -----------------------------------
-        long long per_head = head_work(A, rq, L.row_tiles, kRows);
-        while (pos >= b_from + per_head * H) {
-            b_from += per_head * H;
+        int per_head = head_work(A, rq, L.row_tiles, kRows);
+        while (pos - b_from >= static_cast<long long>(per_head) * H) {
+            b_from += static_cast<long long>(per_head) * H;
             rq = request(A, ++b);
             per_head = head_work(A, rq, L.row_tiles, kRows);
         }
-        const int h = static_cast<int>((pos - b_from) / per_head);
-        const long long h_from = b_from + h * per_head;
+        const unsigned in_req = static_cast<unsigned>(pos - b_from);
+        const int h = in_req / static_cast<unsigned>(per_head);
+        const int in_head = in_req - static_cast<unsigned>(h) * per_head;
         const int live = (rq.rows * A.G + kRows - 1) / kRows;
         const int visited = rq.visited();
-        const long long in_head = pos - h_from;
-        int rt, nt_unit;
-        long long u_from;
-        if (in_head < static_cast<long long>(live) * visited) {
-            rt = static_cast<int>(in_head / visited);
-            nt_unit = visited;
-            u_from = h_from + static_cast<long long>(rt) * visited;
+        int rt, tiles_u, v0;                    // block of rows, tiles of the unit, the first of them here
+        if (in_head < live * visited) {
+            rt = static_cast<unsigned>(in_head) / static_cast<unsigned>(visited);
+            tiles_u = visited;
+            v0 = in_head - rt * visited;
         } else {
-            rt = live + static_cast<int>(in_head - static_cast<long long>(live) * visited);
-            nt_unit = 1;
-            u_from = pos;
+            rt = live + in_head - live * visited;
+            tiles_u = 1;
+            v0 = 0;
         }
-        const int v0 = static_cast<int>(pos - u_from);
-        const int v1 = static_cast<int>(min(static_cast<long long>(nt_unit), hi - u_from));
+        const long long u_from = pos - v0;
+        const int v1 = static_cast<int>(min(static_cast<long long>(tiles_u), hi - u_from));
         const int row0 = rt * kRows;
         const int live_rows = min(max(rq.rows * A.G - row0, 0), kRows);
+        const int tiles = live_rows > 0 ? v1 - v0 : 0;
 
-        // ---- page ids: a lane per page block of the coming tiles ------------
+        // ---- copies: warp 0, a lane per page block of the coming tiles -------
         int entry = -2;
-        auto load_entries = [&](int k0) {
-            const int v = v0 + warp + kAtWarps * (k0 + lane / ppt);
+        uint32_t fifo = 0;                      // (all warps) per tile in flight: which page blocks are there
+        auto entries = [&](int k0) {
+            const int v = v0 + k0 + (lane >> ppt_shift);
             entry = -2;
             if (v < v1) {
-                const int t = rq.real(v) * kTile + ((lane % ppt) << p_shift);
-                const bool need = t < rq.len && (A.window == 0 || t < A.sinks || t + P > rq.low);
-                if (need) {
+                const int t = rq.real(v) * kTile + ((lane & (ppt - 1)) << p_shift);
+                if (t < rq.len && (A.window == 0 || t < A.sinks || t + P > rq.low)) {
                     entry = cache_page(A.tab, A.pool.num_pages, p_shift, b, t);
-                    if (entry < 0 && A.status) atomicOr(A.status + b, SPEC_ST_BAD_PAGE);
+                    if (entry < 0 && A.status && warp == 0) atomicOr(A.status + b, SPEC_ST_BAD_PAGE);
                 }
             }
         };
-        uint32_t fifo = 0;                      // per tile in flight: which page blocks are there
-        const int tiles = live_rows > 0 && v1 - v0 > warp ? (v1 - v0 - warp + kAtWarps - 1) / kAtWarps : 0;   // this warp's
         auto issue = [&](int k, int s, int depth) {
-            if (k % per == 0) load_entries(k);
-            const int g = (k % per) * ppt;
+            const int in = k & ((32 >> ppt_shift) - 1);     // of the tiles whose page ids the lanes hold
+            if (in == 0) entries(k);
+            const int g = in << ppt_shift;
             const unsigned got = __ballot_sync(0xffffffffu, entry >= 0);
             const uint32_t there = (got >> g) & ((1u << ppt) - 1u);
             fifo |= there << (4 * depth);
-            if (!dead) {
-                if (lane == 0) mbar_expect_tx(&full[warp][s], __popc(there) * block_bytes);
+            if (warp == 0) {
+                if (lane == 0) mbar_expect_tx(&full[s], __popc(there) * block_bytes);
                 __syncwarp();
                 if (lane >= g && lane < g + ppt && entry >= 0)
-                    tma_load_1d(ring + s * Cfg::kStageBytes + (lane - g) * block_bytes,
-                                A.pool.base + entry * A.pool.page_stride + h * A.pool.head_stride, block_bytes,
-                                &full[warp][s]);
+                    tma_load_1d(smem + s * Cfg::kStageBytes + (lane - g) * block_bytes,
+                                A.pool.base + entry * A.pool.page_stride + h * A.pool.head_stride, block_bytes, &full[s]);
             }
         };
+        if (!s_dead)
 #pragma unroll
-        for (int s = 0; s < kS; ++s)
-            if (s < tiles) issue(s, s, s);
+            for (int s = 0; s < kS; ++s)
+                if (s < tiles) issue(s, s, s);
 
         // ---- Q, laid out like the keys' words -------------------------------
-        uint32_t qf[NT][D / 16][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int rho = row0 + nt * 8 + r8;
-            const bool on = nt * 8 + r8 < live_rows;
-            const int i = on ? rho / A.G : 0, g = on ? rho % A.G : 0;
-            const uint16_t* q = A.q + b * A.q_bs + i * A.q_rs + (static_cast<long long>(h) * A.G + g) * A.q_hs +
-                                c4 * (D / 4);
-#pragma unroll
-            for (int w = 0; w < kKW; ++w) {
-                uint32_t x[4] = {0, 0, 0, 0};
-                if (on) {
+        if (tid < kRows) {
+            const int rho = row0 + tid, i = rho / A.G, g = rho - i * A.G;
+            const long long head = static_cast<long long>(h) * A.G + g;
+            s_q[tid] = tid < live_rows ? b * A.q_bs + i * A.q_rs + head * A.q_hs : 0;
+            s_out[tid] = rho < A.n * A.G ? (static_cast<long long>(b) * A.n + i) * A.hq + head : -1;
+        }
+        __syncthreads();
+        if (tiles > 0)
+            for (int x = tid; x < NT * kKW * 32; x += kAtThreads) {
+                const int l = x & 31, nt = (x >> 5) % NT, w = (x >> 5) / NT;
+                const int row = nt * 8 + (l >> 2);
+                uint32_t y[4] = {0, 0, 0, 0};
+                if (row < live_rows) {
+                    const uint16_t* q = A.q + s_q[row] + (l & 3) * (D / 4) + 8 * w;
                     if (A.aligned) {
-                        const uint4 t = *reinterpret_cast<const uint4*>(q + 8 * w);
-                        x[0] = t.x; x[1] = t.y; x[2] = t.z; x[3] = t.w;
+                        const uint4 t = *reinterpret_cast<const uint4*>(q);
+                        y[0] = t.x; y[1] = t.y; y[2] = t.z; y[3] = t.w;
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) x[e] = q[8 * w + 2 * e] | (static_cast<uint32_t>(q[8 * w + 2 * e + 1]) << 16);
+                        for (int e = 0; e < 4; ++e) y[e] = q[2 * e] | (static_cast<uint32_t>(q[2 * e + 1]) << 16);
                     }
                 }
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    qf[nt][2 * w + u][0] = __byte_perm(x[u], x[u + 2], 0x5410);
-                    qf[nt][2 * w + u][1] = __byte_perm(x[u], x[u + 2], 0x7632);
-                }
+                for (int u = 0; u < 2; ++u)
+                    sts64(q_base + (((2 * w + u) * NT + nt) * 32 + l) * 8, __byte_perm(y[u], y[u + 2], 0x5410),
+                          __byte_perm(y[u], y[u + 2], 0x7632));
             }
+        __syncthreads();
+        uint32_t qf[Cfg::kQInRegs ? D / 16 : 1][NT][2];
+        if constexpr (Cfg::kQInRegs) {
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) lds(qf[ks][nt], q_base + ((ks * NT + nt) * 32 + lane) * 8);
         }
 
-        float o[kMT][NT][4], m[NT][2], l[NT][2], lr[NT][4];
+        // The sums of rounded weights are a row of ones times P^T; warp w keeps
+        // those of the column blocks w, w + 4, ...
+        constexpr int kLR = (NT + 3) / 4;
+        float o[kMT][NT][4], m[NT][2], l[NT][2], lr[kLR][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             m[nt][0] = m[nt][1] = kNoMax;
             l[nt][0] = l[nt][1] = 0.0f;
-            lr[nt][0] = lr[nt][1] = lr[nt][2] = lr[nt][3] = 0.0f;
 #pragma unroll
             for (int j = 0; j < kMT; ++j) o[j][nt][0] = o[j][nt][1] = o[j][nt][2] = o[j][nt][3] = 0.0f;
         }
-        const float cs = A.scale * kLog2e * 16.0f;
+
+#pragma unroll
+        for (int q = 0; q < kLR; ++q) lr[q][0] = lr[q][1] = lr[q][2] = lr[q][3] = 0.0f;
 
         // ---- the tiles -------------------------------------------------------
-        int s = 0;
+        int s = 0, refill = kS - 1;             // this tile's stage, the one before it
         for (int k = 0; k < tiles; ++k) {
-            const int t0 = rq.real(v0 + warp + kAtWarps * k) * kTile;
+            const int t0 = rq.real(v0 + k) * kTile;
             const uint32_t there = fifo & 15u;
             fifo >>= 4;
-            if (!dead) {
-                uint32_t ph = 0;
-#pragma unroll
-                for (int q = 0; q < kS; ++q)
-                    if (q == s) { ph = phase[q]; phase[q] ^= 1u; }
-                if (!mbar_wait(&full[warp][s], ph)) {
-                    dead = true;
-                    if (lane == 0) atomicOr(&L.ctrl->error, SPEC_WS_ERR_WAIT);
-                }
-                dead = __any_sync(0xffffffffu, dead);
+            if (!s_dead && !mbar_wait(&full[s], (phases >> s) & 1u)) {
+                s_dead = 1;
+                atomicOr(&L.ctrl->error, SPEC_WS_ERR_WAIT);
             }
-            // which keys this warp's rows see; every key of most tiles
+            phases ^= 1u << s;
+            const uint32_t stage = ring + s * Cfg::kStageBytes;
+            const uint32_t pbuf = p_base + (k & 1) * Cfg::kP;
+            // every row sees every key of most tiles
             const bool masked = t0 + kTile > rq.ctx || there != (1u << ppt) - 1u ||
                                 (A.window > 0 && t0 + kTile > A.sinks && t0 < rq.low + A.n);
-            unsigned long long seen = 0, any = ~0ull;
-            if (masked) {
-                if (lane < live_rows) seen = seen64(A, rq, b, (row0 + lane) / A.G, t0);
-#pragma unroll 1
-                for (int q = 0; q < ppt; ++q)
-                    if (!(there >> q & 1u)) seen &= ~range64(q << p_shift, (q + 1) << p_shift, 0);
-                any = seen;
-                any = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(any)) |
-                      static_cast<unsigned long long>(__reduce_or_sync(0xffffffffu, static_cast<uint32_t>(any >> 32))) << 32;
-            }
-            const uint32_t stage = ring_u32 + s * Cfg::kStageBytes;
-            auto part = [&](auto is_masked, int g) {
+            auto tile = [&](auto is_masked) {
                 constexpr bool kMasked = decltype(is_masked)::value;
-                float x[kMB][NT][4];
-                // S^T = K Q^T
+                unsigned long long any = ~0ull;
+                if constexpr (kMasked) {
+                    if (tid < kRows) {
+                        unsigned long long v = 0;
+                        if (tid < live_rows) v = seen64(A, rq, b, (row0 + tid) / A.G, t0);
+#pragma unroll 1
+                        for (int q = 0; q < ppt; ++q)
+                            if (!(there >> q & 1u)) v &= ~range64(q << p_shift, (q + 1) << p_shift, 0);
+                        s_seen[tid] = v;
+                    }
+                    __syncthreads();
+                    any = 0;
+                    for (int q = lane; q < kRows; q += 32) any |= s_seen[q];
+                    any = __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(any)) |
+                          static_cast<unsigned long long>(
+                              __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(any >> 32))) << 32;
+                }
+                // S^T = K Q^T: this warp's 16 tokens
+                float x[NT][4];
 #pragma unroll
-                for (int mb = 0; mb < kMB; ++mb) {
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) x[mb][nt][0] = x[mb][nt][1] = x[mb][nt][2] = x[mb][nt][3] = 0.0f;
-                    const int t = (g * kMB + mb) * 16, slot = t & (P - 1);
-                    const uint32_t blk = stage + (t >> p_shift) * block_bytes;
-                    const uint32_t kr = blk + slot * Blk::kRow + k_at, sc = blk + slot * Blk::kScl + ks_at;
+                for (int nt = 0; nt < NT; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.0f;
+                {
                     uint32_t wa[kKW], wb[kKW];
-                    lds(wa, kr);
-                    lds(wb, kr + 8 * Blk::kRow);
-                    const uint32_t sa = lds16(sc) * 0x10001u, sb = lds16(sc + 8 * Blk::kScl) * 0x10001u;
+                    lds(wa, stage + k_at);
+                    lds(wb, stage + k_at + 8 * Blk::kRow);
+                    const uint32_t sa = lds16(stage + ks_at) * 0x10001u, sb = lds16(stage + ks_at + 8 * Blk::kScl) * 0x10001u;
                     const uint32_t ca = minus1_5(sa), cb = minus1_5(sb);
+                    auto step = [&](int ks, const uint32_t (&a)[4]) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            if constexpr (Cfg::kQInRegs) {
+                                mma(x[nt], a, qf[ks][nt][0], qf[ks][nt][1]);
+                            } else {
+                                uint32_t q2[2];
+                                lds(q2, q_base + ((ks * NT + nt) * 32 + lane) * 8);
+                                mma(x[nt], a, q2[0], q2[1]);
+                            }
+                        }
+                    };
 #pragma unroll
                     for (int w = 0; w < kKW; ++w) {
                         const uint32_t a0[4] = {codes2<0>(wa[w], sa, ca), codes2<0>(wb[w], sb, cb),
                                                 codes2<1>(wa[w], sa, ca), codes2<1>(wb[w], sb, cb)};
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma(x[mb][nt], a0, qf[nt][2 * w][0], qf[nt][2 * w][1]);
+                        step(2 * w, a0);
                         const uint32_t a1[4] = {codes2<2>(wa[w], sa, ca), codes2<2>(wb[w], sb, cb),
                                                 codes2<3>(wa[w], sa, ca), codes2<3>(wb[w], sb, cb)};
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma(x[mb][nt], a1, qf[nt][2 * w + 1][0], qf[nt][2 * w + 1][1]);
+                        step(2 * w + 1, a1);
                     }
                 }
                 if constexpr (kMasked) {
@@ -496,98 +539,98 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const int row = nt * 8 + 2 * c4 + e;
-                            const unsigned long long v =
-                                __shfl_sync(0xffffffffu, seen, row) >> (g * kMB * 16 + tok);
-#pragma unroll
-                            for (int mb = 0; mb < kMB; ++mb) {
-                                if (!(v >> (16 * mb) & 1)) x[mb][nt][e] = -CUDART_INF_F;
-                                if (!(v >> (16 * mb + 8) & 1)) x[mb][nt][2 + e] = -CUDART_INF_F;
-                            }
+                            const uint32_t v = static_cast<uint32_t>(s_seen[nt * 8 + 2 * c4 + e] >> (warp * 16 + tok));
+                            if (!(v & 1u)) x[nt][e] = -CUDART_INF_F;
+                            if (!(v >> 8 & 1u)) x[nt][2 + e] = -CUDART_INF_F;
                         }
                 }
-                // the running maximum, moved only when it must be
+                // Weights under the maximum so far, as the 16 x 8 operand P^T.
+                // They are rounded to bf16 for the tensor cores (2^-8 each at
+                // most, as the output's own rounding); lse takes their sum
+                // before that, the output is divided by the sum of the rounded
+                // ones, so that what rounding they have in common cancels (one
+                // dominant key: all of it).  A tile with masked keys, where a
+                // row may see only a few, adds a second term with what rounding
+                // took from the first.
+                float ls[NT][2];
+                auto weights = [&]() {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float p[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) p[e] = exp2_fast(fmaf(x[nt][e], cs, -m[nt][e & 1]));
+                        ls[nt][0] = p[0] + p[2];
+                        ls[nt][1] = p[1] + p[3];
+                        const uint32_t ab = pack_bf16(p[0], p[1]), cd = pack_bf16(p[2], p[3]);
+                        sts64(pbuf + ((warp * NT + nt) * 32 + lane) * 8, transpose8x8(ab), transpose8x8(cd));
+                        if constexpr (kMasked) {
+                            const uint32_t rab = pack_bf16(p[0] - __uint_as_float(ab << 16),
+                                                           p[1] - __uint_as_float(ab & 0xffff0000u));
+                            const uint32_t rcd = pack_bf16(p[2] - __uint_as_float(cd << 16),
+                                                           p[3] - __uint_as_float(cd & 0xffff0000u));
+                            sts64(lo_base + ((warp * NT + nt) * 32 + lane) * 8, transpose8x8(rab), transpose8x8(rcd));
+                        }
+                    }
+                };
                 bool move = false;
-                float top[NT][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float t = fmaxf(x[0][nt][e], x[0][nt][2 + e]);
-#pragma unroll
-                        for (int mb = 1; mb < kMB; ++mb) t = fmaxf(t, fmaxf(x[mb][nt][e], x[mb][nt][2 + e]));
-                        top[nt][e] = t * cs;
-                        move |= top[nt][e] > m[nt][e] + kSlack;
-                    }
-                if (__any_sync(0xffffffffu, move)) {
+                    for (int e = 0; e < 2; ++e)
+                        move |= fmaxf(x[nt][e], x[nt][2 + e]) * cs > m[nt][e] + kSlack;
+                weights();
+                if (__syncthreads_or(move)) {
+                    // the maximum moves: all warps agree on it, rescale, and weigh again
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            float t = top[nt][e];
+                            float t = fmaxf(x[nt][e], x[nt][2 + e]) * cs;
                             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
                             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
                             t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-                            const float mn = fmaxf(m[nt][e], t);
+                            if (r8 == 0) s_max[warp][nt * 8 + 2 * c4 + e] = t;
+                        }
+                    __syncthreads();
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float mn = m[nt][e];
+#pragma unroll
+                            for (int w = 0; w < kAtWarps; ++w) mn = fmaxf(mn, s_max[w][nt * 8 + 2 * c4 + e]);
                             const float f = exp2_fast(m[nt][e] - mn);
                             m[nt][e] = mn;
                             l[nt][e] *= f;
-                            lr[nt][e] *= f;
+                            if ((nt & 3) == warp) lr[nt >> 2][e] *= f;
 #pragma unroll
                             for (int j = 0; j < kMT; ++j) {
                                 o[j][nt][e] *= f;
                                 o[j][nt][2 + e] *= f;
                             }
                         }
+                    weights();
+                    __syncthreads();
                 }
-                // weights, as the 16 x 8 operand P^T.  They are rounded to bf16
-                // for the tensor cores (2^-8 each at most, as the output's own
-                // rounding); lse takes their sum before that, the output is
-                // divided by the sum of the rounded ones, so that what rounding
-                // they have in common cancels (one dominant key: all of it).
-                // A tile with masked keys, where a row may see only a few, adds a
-                // second term with what rounding took from the first.
-                uint32_t pf[kMB][NT][2], pl[kMasked ? kMB : 1][NT][2];
-#pragma unroll
-                for (int mb = 0; mb < kMB; ++mb)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        float p[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) p[e] = exp2_fast(fmaf(x[mb][nt][e], cs, -m[nt][e & 1]));
-                        l[nt][0] += p[0] + p[2];
-                        l[nt][1] += p[1] + p[3];
-                        const uint32_t lo = pack_bf16(p[0], p[1]), hi = pack_bf16(p[2], p[3]);
-                        pf[mb][nt][0] = transpose8x8(lo);
-                        pf[mb][nt][1] = transpose8x8(hi);
-                        if constexpr (kMasked) {
-                            pl[mb][nt][0] = transpose8x8(pack_bf16(p[0] - __uint_as_float(lo << 16),
-                                                                   p[1] - __uint_as_float(lo & 0xffff0000u)));
-                            pl[mb][nt][1] = transpose8x8(pack_bf16(p[2] - __uint_as_float(hi << 16),
-                                                                   p[3] - __uint_as_float(hi & 0xffff0000u)));
-                        }
-                    }
-                // O^T += V^T P^T, and a row of ones for the sum
+                // every warp is past the tile before this one: its stage is free
+                if (k > 0 && k - 1 + kS < tiles && !s_dead) issue(k - 1 + kS, refill, kS - 2);
                 const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
 #pragma unroll
-                for (int mb = 0; mb < kMB; ++mb) {
+                for (int nt = 0; nt < NT; ++nt) {
+                    l[nt][0] += ls[nt][0];
+                    l[nt][1] += ls[nt][1];
+                }
+                // O^T += V^T P^T: this warp's rows, all tokens
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma(lr[nt], ones, pf[mb][nt][0], pf[mb][nt][1]);
-                        if constexpr (kMasked) mma(lr[nt], ones, pl[mb][nt][0], pl[mb][nt][1]);
-                    }
-                    const int t = (g * kMB + mb) * 16, slot = t & (P - 1);
-                    const uint32_t blk = stage + (t >> p_shift) * block_bytes;
-                    const uint32_t vr = blk + slot * Blk::kRow, vs = blk + slot * Blk::kScl;
-                    uint32_t w0[kVW], w1[kVW], w2[kVW], w3[kVW];
-                    lds(w0, vr + v0_at);
-                    lds(w1, vr + v1_at);
-                    lds(w2, vr + v0_at + 8 * Blk::kRow);
-                    lds(w3, vr + v1_at + 8 * Blk::kRow);
+                for (int mb = 0; mb < 4; ++mb) {
+                    const uint32_t vr = stage + at16(mb, Blk::kRow), vs = stage + at16(mb, Blk::kScl);
+                    // token pairs side by side: four (two) codes each
+                    const uint32_t ab = __byte_perm(ldsv<D>(vr + v0_at), ldsv<D>(vr + v1_at), 0x5410);
+                    const uint32_t cd = __byte_perm(ldsv<D>(vr + v0_at + 8 * Blk::kRow), ldsv<D>(vr + v1_at + 8 * Blk::kRow), 0x5410);
                     uint32_t s0 = lds16(vs + vs0_at), s1 = lds16(vs + vs1_at);
                     uint32_t s2 = lds16(vs + vs0_at + 8 * Blk::kScl), s3 = lds16(vs + vs1_at + 8 * Blk::kScl);
                     if constexpr (kMasked) {    // what no row sees may be anything, NaN among it
-                        const uint32_t a = static_cast<uint32_t>(any >> t);
+                        const uint32_t a = static_cast<uint32_t>(any >> (mb * 16));
                         s0 = a >> tv0 & 1 ? s0 : 0;
                         s1 = a >> tv1 & 1 ? s1 : 0;
                         s2 = a >> (tv0 + 8) & 1 ? s2 : 0;
@@ -595,46 +638,41 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
                     }
                     const uint32_t sa = s0 | s1 << 16, sb = s2 | s3 << 16;
                     const uint32_t ca = minus1_5(sa), cb = minus1_5(sb);
+                    uint32_t a[kMT][4];
+                    a[0][0] = codes2<0>(ab, sa, ca);
+                    a[0][1] = codes2<1>(ab, sa, ca);
+                    a[0][2] = codes2<0>(cd, sb, cb);
+                    a[0][3] = codes2<1>(cd, sb, cb);
+                    if constexpr (kMT == 2) {
+                        a[1][0] = codes2<2>(ab, sa, ca);
+                        a[1][1] = codes2<3>(ab, sa, ca);
+                        a[1][2] = codes2<2>(cd, sb, cb);
+                        a[1][3] = codes2<3>(cd, sb, cb);
+                    }
 #pragma unroll
-                    for (int w = 0; w < kVW; ++w) {
-                        // token pairs side by side: elements 0..3 and 4..7 of the word
-                        const uint32_t a_lo = __byte_perm(w0[w], w1[w], 0x5410), a_hi = __byte_perm(w0[w], w1[w], 0x7632);
-                        const uint32_t b_lo = __byte_perm(w2[w], w3[w], 0x5410), b_hi = __byte_perm(w2[w], w3[w], 0x7632);
-#define SPEC_PV(I)                                                                                        \
-    {                                                                                                     \
-        const uint32_t a[4] = {codes2<I>(a_lo, sa, ca), codes2<I>(a_hi, sa, ca), codes2<I>(b_lo, sb, cb), \
-                               codes2<I>(b_hi, sb, cb)};                                                  \
-        _Pragma("unroll") for (int nt = 0; nt < NT; ++nt) {                                               \
-            mma(o[4 * w + I][nt], a, pf[mb][nt][0], pf[mb][nt][1]);                                       \
-            if constexpr (kMasked) mma(o[4 * w + I][nt], a, pl[mb][nt][0], pl[mb][nt][1]);                \
-        }                                                                                                 \
-    }
-                        SPEC_PV(0)
-                        SPEC_PV(1)
-                        SPEC_PV(2)
-                        SPEC_PV(3)
-#undef SPEC_PV
+                    for (int nt = 0; nt < NT; ++nt) {
+                        uint32_t p2[2];
+                        lds(p2, pbuf + ((mb * NT + nt) * 32 + lane) * 8);
+#pragma unroll
+                        for (int j = 0; j < kMT; ++j) mma(o[j][nt], a[j], p2[0], p2[1]);
+                        if ((nt & 3) == warp) mma(lr[nt >> 2], ones, p2[0], p2[1]);
+                        if constexpr (kMasked) {
+                            lds(p2, lo_base + ((mb * NT + nt) * 32 + lane) * 8);
+#pragma unroll
+                            for (int j = 0; j < kMT; ++j) mma(o[j][nt], a[j], p2[0], p2[1]);
+                            if ((nt & 3) == warp) mma(lr[nt >> 2], ones, p2[0], p2[1]);
+                        }
                     }
                 }
+                if constexpr (kMasked) __syncthreads();     // the second terms' buffer is written again
             };
-            if (masked) {
-#pragma unroll 1
-                for (int g = 0; g < 4 / kMB; ++g) part(std::true_type{}, g);
-            } else {
-#pragma unroll 1
-                for (int g = 0; g < 4 / kMB; ++g) part(std::false_type{}, g);
-            }
-            __syncwarp();
-            if (k + kS < tiles) issue(k + kS, s, kS - 1);
+            if (masked) tile(std::true_type{});
+            else tile(std::false_type{});
+            refill = s;
             s = s + 1 == kS ? 0 : s + 1;
         }
 
-        // ---- join the warps ---------------------------------------------------
-        // value (row d of O^T): d = (D/8) r8 + 8 w + i (+4) lies in block j = 4w + i;
-        // it is stored at place (half * kMT + j) * 8 + r8
-        __syncthreads();                        // every warp is done with its ring
-        float* jo = reinterpret_cast<float*>(smem);                         // [warp][row][kPad]
-        float* jm = jo + kAtWarps * kRows * kPad;                           // [warp][row][3]: m, l, l of the rounded weights
+        // ---- the rows' sums, and out -------------------------------------------
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -643,20 +681,11 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
                 t += __shfl_xor_sync(0xffffffffu, t, 4);
                 t += __shfl_xor_sync(0xffffffffu, t, 8);
                 t += __shfl_xor_sync(0xffffffffu, t, 16);
-                const int row = warp * kRows + nt * 8 + 2 * c4 + e;
-                if (r8 == 0) {
-                    jm[row * 3] = m[nt][e];
-                    jm[row * 3 + 1] = t;
-                    jm[row * 3 + 2] = lr[nt][e];
-                }
-#pragma unroll
-                for (int j = 0; j < kMT; ++j) {
-                    jo[row * kPad + j * 8 + r8] = o[j][nt][e];
-                    jo[row * kPad + (kMT + j) * 8 + r8] = o[j][nt][2 + e];
-                }
+                if (r8 == 0) s_l[warp][nt * 8 + 2 * c4 + e] = t;
+                if (r8 == 0 && (nt & 3) == warp) s_lr[nt * 8 + 2 * c4 + e] = lr[nt >> 2][e];
             }
         __syncthreads();
-        const bool whole = v0 == 0 && v1 == nt_unit;
+        const bool whole = v0 == 0 && v1 == tiles_u;
         // the CTA that holds the unit's first tile, and how many share it
         int c0 = cta, parts = 1;
         if (!whole) {
@@ -666,54 +695,50 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
                 while (start_of(c) > x) --c;
                 return c;
             };
-            c0 = cta_of(u_from);
-            parts = cta_of(u_from + nt_unit - 1) - c0 + 1;
+            c0 = v0 == 0 ? cta : cta_of(u_from);
+            parts = (v1 == tiles_u ? cta : cta_of(u_from + tiles_u - 1)) - c0 + 1;
         }
         const int slot = 2 * cta + (c0 == cta ? 1 : 0);
-        // An item is eight neighbouring values of a row: (row, r8, w).
-        constexpr int kItems = kRows * (D / 8);
-        const int rows_here = min(kRows, A.n * A.G - row0);     // rows of the output in this block
-        auto emit = [&](int row, int item, const float (&v)[8], float mm, float ls, float lrs) {
-            const int rho = row0 + row, i = rho / A.G, g = rho % A.G;
-            const long long at = (static_cast<long long>(b) * A.n + i) * A.hq + static_cast<long long>(h) * A.G + g;
-            const bool on = row < live_rows && ls != 0.0f;
-            const float f = on ? 16.0f / lrs : 0.0f;
-            uint4 u;
-            u.x = on ? pack_bf16(v[0] * f, v[1] * f) : 0;
-            u.y = on ? pack_bf16(v[2] * f, v[3] * f) : 0;
-            u.z = on ? pack_bf16(v[4] * f, v[5] * f) : 0;
-            u.w = on ? pack_bf16(v[6] * f, v[7] * f) : 0;
-            *reinterpret_cast<uint4*>(A.out + at * D + item * 8) = u;
-            if (A.lse && item == 0) A.lse[at] = on ? (mm + log2f(ls)) * kLn2 : -CUDART_INF_F;
+        const int d0 = warp * (D / 4) + r8 * (D / 32);          // this lane's D/32 values of a row
+        auto emit = [&](int row, const float (&v)[2 * kMT], float mm, float sum, float rsum) {
+            const long long at = s_out[row];
+            if (at < 0) return;
+            const bool on = row < live_rows && sum != 0.0f;
+            const float f = on ? 16.0f / rsum : 0.0f;
+            uint32_t u[kMT];
+#pragma unroll
+            for (int j = 0; j < kMT; ++j) u[j] = on ? pack_bf16(v[2 * j] * f, v[2 * j + 1] * f) : 0;
+            uint16_t* to = A.out + at * D + d0;
+            if constexpr (kMT == 2) *reinterpret_cast<uint2*>(to) = make_uint2(u[0], u[1]);
+            else *reinterpret_cast<uint32_t*>(to) = u[0];
+            if (A.lse && warp == 0 && r8 == 0) A.lse[at] = on ? (mm + log2f(sum)) * kLn2 : -CUDART_INF_F;
         };
 #pragma unroll
-        for (int x = tid; x < kItems; x += kAtThreads) {
-            const int row = x / (D / 8), item = x % (D / 8);    // values 8 item .. 8 item + 7 of the row
-            const int rr = item / kVW, w8 = item % kVW;
-            float mm = kNoMax;
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int w = 0; w < kAtWarps; ++w) mm = fmaxf(mm, jm[(w * kRows + row) * 3]);
-            float v[8] = {}, ls = 0.0f, lrs = 0.0f;
+            for (int e = 0; e < 2; ++e) {
+                const int row = nt * 8 + 2 * c4 + e;
+                float sum = 0.0f, v[2 * kMT];
+                const float rsum = s_lr[row];
 #pragma unroll
-            for (int w = 0; w < kAtWarps; ++w) {
-                const float* ml = jm + (w * kRows + row) * 3;
-                const float f = exp2_fast(ml[0] - mm);
-                ls += f * ml[1];
-                lrs += f * ml[2];
-                const float* src = jo + (w * kRows + row) * kPad + w8 * 32 + rr;
+                for (int w = 0; w < kAtWarps; ++w) sum += s_l[w][row];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] += f * src[(e >= 4 ? kMT * 8 : 0) + (e & 3) * 8];
+                for (int j = 0; j < kMT; ++j) {
+                    v[2 * j] = o[j][nt][e];
+                    v[2 * j + 1] = o[j][nt][2 + e];
+                }
+                if (whole) {
+                    emit(row, v, m[nt][e], sum, rsum);
+                } else {
+                    const long long at = static_cast<long long>(slot) * kRows + row;
+                    if constexpr (kMT == 2)
+                        __stcg(reinterpret_cast<float4*>(L.part + at * D + d0), make_float4(v[0], v[1], v[2], v[3]));
+                    else
+                        __stcg(reinterpret_cast<float2*>(L.part + at * D + d0), make_float2(v[0], v[1]));
+                    if (warp == 0 && r8 == 0)
+                        __stcg(reinterpret_cast<float4*>(L.ml) + at, make_float4(m[nt][e], sum, rsum, 0.0f));
+                }
             }
-            if (whole) {
-                if (row < rows_here) emit(row, item, v, mm, ls, lrs);
-            } else {
-                float4* to = reinterpret_cast<float4*>(L.part + (static_cast<long long>(slot) * kRows + row) * D + item * 8);
-                __stcg(to, make_float4(v[0], v[1], v[2], v[3]));
-                __stcg(to + 1, make_float4(v[4], v[5], v[6], v[7]));
-                if (item == 0)
-                    __stcg(reinterpret_cast<float4*>(L.ml) + slot * kRows + row, make_float4(mm, ls, lrs, 0.0f));
-            }
-        }
         if (!whole) {
             __threadfence();
             __syncthreads();
@@ -725,31 +750,33 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
             __syncthreads();
             if (s_last) {
                 __threadfence();
-                for (int x = tid; x < rows_here * (D / 8); x += kAtThreads) {
-                    const int row = x / (D / 8), item = x % (D / 8);
+#pragma unroll 1
+                for (int ne = 0; ne < 2 * NT; ++ne) {
+                    const int row = (ne >> 1) * 8 + 2 * c4 + (ne & 1);
                     auto place = [&](int c) { return (2ll * (c0 + c) + (c == 0 ? 1 : 0)) * kRows + row; };
                     float mm = kNoMax;
 #pragma unroll 4
                     for (int c = 0; c < parts; ++c) mm = fmaxf(mm, __ldcg(L.ml + place(c) * 4));
-                    float v[8] = {}, ls = 0.0f, lrs = 0.0f;
+                    float v[2 * kMT] = {}, sum = 0.0f, rsum = 0.0f;
 #pragma unroll 4
                     for (int c = 0; c < parts; ++c) {
                         const float4 ml = __ldcg(reinterpret_cast<const float4*>(L.ml) + place(c));
-                        const float4* from = reinterpret_cast<const float4*>(L.part + place(c) * D + item * 8);
-                        const float4 a = __ldcg(from), z = __ldcg(from + 1);
                         const float f = exp2_fast(ml.x - mm);
-                        ls += f * ml.y;
-                        lrs += f * ml.z;
-                        v[0] += f * a.x; v[1] += f * a.y; v[2] += f * a.z; v[3] += f * a.w;
-                        v[4] += f * z.x; v[5] += f * z.y; v[6] += f * z.z; v[7] += f * z.w;
+                        sum += f * ml.y;
+                        rsum += f * ml.z;
+                        if constexpr (kMT == 2) {
+                            const float4 z = __ldcg(reinterpret_cast<const float4*>(L.part + place(c) * D + d0));
+                            v[0] += f * z.x; v[1] += f * z.y; v[2] += f * z.z; v[3] += f * z.w;
+                        } else {
+                            const float2 z = __ldcg(reinterpret_cast<const float2*>(L.part + place(c) * D + d0));
+                            v[0] += f * z.x; v[1] += f * z.y;
+                        }
                     }
-                    emit(row, item, v, mm, ls, lrs);
+                    emit(row, v, mm, sum, rsum);
                 }
             }
         }
-        // the ring is copied into again: order the joins' accesses before it
-        fence_proxy_async_smem();
-        __syncthreads();
+        __syncthreads();                        // shared memory is written again
         pos = u_from + v1;
     }
 }
@@ -763,8 +790,16 @@ int sm_count() {
     return v;
 }
 
-// blocks of 8 rows a warp holds at once
-int row_blocks(int R) { return R <= 8 ? 1 : 2; }
+// Blocks of 8 rows that a CTA holds at once.  The whole of R where it fits: a
+// tile's codes are decoded once for all rows.  Beyond 12 blocks, what the registers hold,
+// the rows are cut into equal parts.
+int row_blocks(int R) {
+    static constexpr int kSizes[] = {1, 2, 3, 4, 5, 6, 8, 12};
+    const int need = (R + 7) / 8, cuts = (need + 11) / 12, each = (need + cuts - 1) / cuts;
+    for (const int s : kSizes)
+        if (s >= each) return s;
+    return 12;
+}
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -779,7 +814,7 @@ Layout layout_of(int grid, int NT, int D) {
     return y;
 }
 
-template <int D, int NT, int P>
+template <int D, int NT>
 cudaError_t attend(const CacheAttendArgs& A, cudaStream_t st) {
     using Cfg = AttendCfg<D, NT>;
     const int grid = min(sm_count() * Cfg::kCtas, kMaxGrid);
@@ -787,16 +822,33 @@ cudaError_t attend(const CacheAttendArgs& A, cudaStream_t st) {
     AttendPlan L;
     L.grid = grid;
     L.row_tiles = (A.n * A.G + Cfg::kRows - 1) / Cfg::kRows;
-    L.min_tiles = 2 * kAtWarps;
+    L.min_tiles = 3;
+    // a request's tiles are counted in 32 bits
+    const long long tiles = ((static_cast<long long>(A.tab.width) << A.pool.p_shift) + A.n) / kTile + 2;
+    if (tiles * A.pool.heads * L.row_tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
     unsigned char* ws = static_cast<unsigned char*>(A.ws);
     L.ctrl = reinterpret_cast<AttendCtrl*>(ws);
     L.ml = reinterpret_cast<float*>(ws + y.ml);
     L.part = reinterpret_cast<float*>(ws + y.part);
-    const cudaError_t e = cudaFuncSetAttribute(cache_attend_kernel<D, NT, P>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(cache_attend_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                Cfg::kSmem);
     if (e != cudaSuccess) return e;
-    cache_attend_kernel<D, NT, P><<<grid, kAtThreads, Cfg::kSmem, st>>>(A, L);
+    cache_attend_kernel<D, NT><<<grid, kAtThreads, Cfg::kSmem, st>>>(A, L);
     return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t attend_rows(const CacheAttendArgs& A, cudaStream_t st) {
+    switch (row_blocks(A.n * A.G)) {
+        case 1: return attend<D, 1>(A, st);
+        case 2: return attend<D, 2>(A, st);
+        case 3: return attend<D, 3>(A, st);
+        case 4: return attend<D, 4>(A, st);
+        case 5: return attend<D, 5>(A, st);
+        case 6: return attend<D, 6>(A, st);
+        case 8: return attend<D, 8>(A, st);
+        default: return attend<D, 12>(A, st);
+    }
 }
 
 }  // namespace
@@ -804,26 +856,11 @@ cudaError_t attend(const CacheAttendArgs& A, cudaStream_t st) {
 size_t cache_attend_ws(int B, int n, int hq, int hkv, int D) {
     (void)B;
     const int NT = row_blocks(n * (hq / hkv));
-    return layout_of(min(sm_count() * 3, kMaxGrid), NT, D).bytes;
+    return layout_of(min(sm_count() * ctas_of(NT), kMaxGrid), NT, D).bytes;
 }
-
-namespace {
-
-template <int D, int NT>
-cudaError_t attend_pages(const CacheAttendArgs& A, cudaStream_t st) {
-    switch (A.pool.P) {
-        case 16: return attend<D, NT, 16>(A, st);
-        case 32: return attend<D, NT, 32>(A, st);
-        default: return attend<D, NT, 64>(A, st);
-    }
-}
-
-}  // namespace
 
 cudaError_t cache_attend_run(const CacheAttendArgs& A, cudaStream_t st) {
-    const int NT = row_blocks(A.n * A.G);
-    if (A.pool.D == 128) return NT == 1 ? attend_pages<128, 1>(A, st) : attend_pages<128, 2>(A, st);
-    return NT == 1 ? attend_pages<64, 1>(A, st) : attend_pages<64, 2>(A, st);
+    return A.pool.D == 128 ? attend_rows<128>(A, st) : attend_rows<64>(A, st);
 }
 
 }  // namespace spec
