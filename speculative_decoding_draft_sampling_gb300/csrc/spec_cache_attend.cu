@@ -81,11 +81,15 @@ struct Req {
     __device__ __forceinline__ int real(int v) const { return v < sink_tiles ? v : first + (v - sink_tiles); }
 };
 
-__device__ __forceinline__ Req request(const CacheAttendArgs& A, int b) {
+// its context and rows as given
+__device__ __forceinline__ int2 request_len(const CacheAttendArgs& A, int b) {
+    return make_int2(A.ctx[b], A.rows ? A.rows[b] : A.n);
+}
+__device__ __forceinline__ Req request(const CacheAttendArgs& A, int2 given) {
     Req r;
     const long long room = static_cast<long long>(A.tab.width) << A.pool.p_shift;
-    r.ctx = static_cast<int>(min(static_cast<long long>(max(A.ctx[b], 0)), room));
-    r.rows = A.rows ? min(max(A.rows[b], 0), A.n) : A.n;
+    r.ctx = static_cast<int>(min(static_cast<long long>(max(given.x, 0)), room));
+    r.rows = min(max(given.y, 0), A.n);
     r.len = r.rows ? r.ctx + r.rows : 0;
     r.tiles = (r.len + kTile - 1) / kTile;
     r.low = 0;
@@ -157,6 +161,11 @@ __device__ __forceinline__ uint32_t ldsv(uint32_t a) {
 __device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
     asm volatile("st.shared.v2.u32 [%0], {%1, %2};" :: "r"(a), "r"(x), "r"(y) : "memory");
 }
+__device__ __forceinline__ void cp_async16(uint32_t to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -252,7 +261,9 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
     __shared__ uint64_t full[kS];
     __shared__ long long s_sum[kAtWarps];
     __shared__ long long s_found[2];
-    __shared__ long long s_q[kRows], s_out[kRows];          // a row's place in q and in out / lse (-1: none)
+    __shared__ int2 s_len[kAtThreads];          // the first requests' lengths
+    __shared__ long long s_out[kRows];          // a row's place in out and lse (-1: none)
+    __shared__ uint32_t s_there[kS];            // which page blocks of a stage's tile are there
     __shared__ unsigned long long s_seen[kRows];
     __shared__ float s_max[kAtWarps][kRows];
     __shared__ float s_l[kAtWarps][kRows], s_lr[kRows];
@@ -264,7 +275,9 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
     const int H = A.pool.heads;
     const int P = A.pool.P, p_shift = A.pool.p_shift;
     const int ppt_shift = 6 - p_shift, ppt = 1 << ppt_shift;    // page blocks a tile
-    const int block_bytes = Blk::bytes(P);
+    // A tile in shared memory is laid out like one block of 64 tokens, whatever
+    // the pages' size.
+    constexpr int kKs = kTile * Blk::kRow, kV = Blk::v_codes(kTile), kVs = kV + kTile * Blk::kRow;
     const uint32_t ring = smem_u32(smem);
     const uint32_t q_base = ring + kS * Cfg::kStageBytes, p_base = q_base + Cfg::kQ, lo_base = p_base + 2 * Cfg::kP;
 
@@ -276,14 +289,20 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
     }
 
     // ---- this CTA's share: [lo, hi) of all tiles ---------------------------
+    int2 given = make_int2(0, 0);
     auto work_of = [&](int b) {
-        return b < A.B ? static_cast<long long>(H) * head_work(A, request(A, b), L.row_tiles, kRows) : 0ll;
+        if (b >= A.B) return 0ll;
+        given = request_len(A, b);
+        return static_cast<long long>(H) * head_work(A, request(A, given), L.row_tiles, kRows);
     };
     // the requests a chunk of threads at a time; one chunk is the usual case
     long long total = 0, first_work = 0;
     for (int b0 = 0; b0 < A.B; b0 += kAtThreads) {
         const long long v = work_of(b0 + tid);
-        if (b0 == 0) first_work = v;
+        if (b0 == 0) {
+            first_work = v;
+            s_len[tid] = given;
+        }
         total += v;
     }
 #pragma unroll
@@ -299,7 +318,11 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
     const int active = static_cast<int>(min(static_cast<long long>(gridDim.x), max(want, 1ll)));
     const int cta = blockIdx.x;
     if (cta >= active) return;
-    auto start_of = [&](long long c) { return c * total / active; };
+    // quotients of 64 bits only where the work needs them
+    auto start_of = [&](long long c) {
+        const long long x = c * total;
+        return x >> 32 ? x / active : static_cast<long long>(static_cast<unsigned>(x) / static_cast<unsigned>(active));
+    };
     const long long lo = start_of(cta), hi = start_of(cta + 1);
     __syncthreads();
     // the request that holds tile lo, and where its tiles start
@@ -333,107 +356,143 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
     }
     int b = static_cast<int>(s_found[0]);
     long long b_from = s_found[1];
-    Req rq = request(A, b);
+    auto req_at = [&](int i) { return request(A, i < kAtThreads ? s_len[i] : request_len(A, i)); };
+    Req rq = req_at(b);
 
     uint32_t phases = 0;                        // one bit a stage
     const int tok = r8 ^ ((r8 >> 1) & 1);       // the token (of 8) that is row r8 of S^T
     const int tv0 = (2 * c4) ^ (c4 & 1);        // tokens 2c and 2c+1 of P^T's rows
     const int tv1 = (2 * c4 + 1) ^ (c4 & 1);
     // where a lane's words and scales lie in a tile: its key (this warp's 16
-    // tokens), and from the start of 16 tokens its part of the values
-    auto at16 = [&](int mb, int row_bytes) {    // rows of the mb-th 16 tokens
-        return ((mb * 16) >> p_shift) * block_bytes + ((mb * 16) & (P - 1)) * row_bytes;
-    };
-    const uint32_t k_at = at16(warp, Blk::kRow) + tok * Blk::kRow + c4 * (D / 8);
-    const uint32_t ks_at = at16(warp, Blk::kScl) + P * Blk::kRow + tok * Blk::kScl + (D == 128 ? c4 : c4 >> 1) * 2;
-    const uint32_t v_at = Blk::v_codes(P) + warp * (D / 8) + r8 * (D / 64);
-    const uint32_t vs_at = Blk::v_codes(P) + P * Blk::kRow + (D == 128 ? warp : warp >> 1) * 2;
+    // tokens), and its part of the values of the first 16
+    const uint32_t k_at = (warp * 16 + tok) * Blk::kRow + c4 * (D / 8);
+    const uint32_t ks_at = kKs + (warp * 16 + tok) * Blk::kScl + (D == 128 ? c4 : c4 >> 1) * 2;
+    const uint32_t v_at = kV + warp * (D / 8) + r8 * (D / 64);
     const uint32_t v0_at = v_at + tv0 * Blk::kRow, v1_at = v_at + tv1 * Blk::kRow;
+    // A lane fetches the scale pair of tokens (2c, 2c+1) of the lane >> 2 -th 8
+    // tokens for the lanes of column c.
+    const uint32_t vs_at = kVs + (lane >> 2) * 8 * Blk::kScl + (D == 128 ? warp : warp >> 1) * 2;
     const uint32_t vs0_at = vs_at + tv0 * Blk::kScl, vs1_at = vs_at + tv1 * Blk::kScl;
     const float cs = A.scale * kLog2e * 16.0f;
 
-    for (long long pos = lo; pos < hi;) {
-        // ---- the unit that holds tile pos -----------------------------------
+    // ---- a unit, or the part of it that falls into this CTA's share ----------
+    struct Seg {
+        int b, h, row0, live_rows;              // request, kv head, first row, rows that are there
+        int v0, v1, tiles_u;                    // tiles [v0, v1) of the unit's
+        int tiles;                              // v1 - v0, or 0 where no row is there
+        long long u_from;                       // the unit's first tile among all
+    };
+    // the unit that holds tile pos (moves rq on to its request)
+    auto segment = [&](long long pos) {
+        Seg g;
         int per_head = head_work(A, rq, L.row_tiles, kRows);
         while (pos - b_from >= static_cast<long long>(per_head) * H) {
             b_from += static_cast<long long>(per_head) * H;
-            rq = request(A, ++b);
+            rq = req_at(++b);
             per_head = head_work(A, rq, L.row_tiles, kRows);
         }
         const unsigned in_req = static_cast<unsigned>(pos - b_from);
-        const int h = in_req / static_cast<unsigned>(per_head);
-        const int in_head = in_req - static_cast<unsigned>(h) * per_head;
+        g.b = b;
+        g.h = in_req / static_cast<unsigned>(per_head);
+        const int in_head = in_req - static_cast<unsigned>(g.h) * per_head;
         const int live = (rq.rows * A.G + kRows - 1) / kRows;
         const int visited = rq.visited();
-        int rt, tiles_u, v0;                    // block of rows, tiles of the unit, the first of them here
+        int rt;
         if (in_head < live * visited) {
             rt = static_cast<unsigned>(in_head) / static_cast<unsigned>(visited);
-            tiles_u = visited;
-            v0 = in_head - rt * visited;
+            g.tiles_u = visited;
+            g.v0 = in_head - rt * visited;
         } else {
             rt = live + in_head - live * visited;
-            tiles_u = 1;
-            v0 = 0;
+            g.tiles_u = 1;
+            g.v0 = 0;
         }
-        const long long u_from = pos - v0;
-        const int v1 = static_cast<int>(min(static_cast<long long>(tiles_u), hi - u_from));
-        const int row0 = rt * kRows;
-        const int live_rows = min(max(rq.rows * A.G - row0, 0), kRows);
-        const int tiles = live_rows > 0 ? v1 - v0 : 0;
-
-        // ---- copies: warp 0, a lane per page block of the coming tiles -------
-        int entry = -2;
-        uint32_t fifo = 0;                      // (all warps) per tile in flight: which page blocks are there
-        auto entries = [&](int k0) {
-            const int v = v0 + k0 + (lane >> ppt_shift);
+        g.u_from = pos - g.v0;
+        g.v1 = static_cast<int>(min(static_cast<long long>(g.tiles_u), hi - g.u_from));
+        g.row0 = rt * kRows;
+        g.live_rows = min(max(rq.rows * A.G - g.row0, 0), kRows);
+        g.tiles = g.live_rows > 0 ? g.v1 - g.v0 : 0;
+        return g;
+    };
+    // Copies, by warp 0: a lane per page block of the coming tiles.
+    int entry = -2;
+    auto issue = [&](const Seg& g, int k, int s) {
+        const int in = k & ((32 >> ppt_shift) - 1);         // of the tiles whose page ids the lanes hold
+        if (in == 0) {
+            const int v = g.v0 + k + (lane >> ppt_shift);
             entry = -2;
-            if (v < v1) {
+            if (v < g.v1) {
                 const int t = rq.real(v) * kTile + ((lane & (ppt - 1)) << p_shift);
                 if (t < rq.len && (A.window == 0 || t < A.sinks || t + P > rq.low)) {
-                    entry = cache_page(A.tab, A.pool.num_pages, p_shift, b, t);
-                    if (entry < 0 && A.status && warp == 0) atomicOr(A.status + b, SPEC_ST_BAD_PAGE);
+                    entry = cache_page(A.tab, A.pool.num_pages, p_shift, g.b, t);
+                    if (entry < 0 && A.status) atomicOr(A.status + g.b, SPEC_ST_BAD_PAGE);
                 }
             }
-        };
-        auto issue = [&](int k, int s, int depth) {
-            const int in = k & ((32 >> ppt_shift) - 1);     // of the tiles whose page ids the lanes hold
-            if (in == 0) entries(k);
-            const int g = in << ppt_shift;
-            const unsigned got = __ballot_sync(0xffffffffu, entry >= 0);
-            const uint32_t there = (got >> g) & ((1u << ppt) - 1u);
-            fifo |= there << (4 * depth);
-            if (warp == 0) {
-                if (lane == 0) mbar_expect_tx(&full[s], __popc(there) * block_bytes);
-                __syncwarp();
-                if (lane >= g && lane < g + ppt && entry >= 0)
-                    tma_load_1d(smem + s * Cfg::kStageBytes + (lane - g) * block_bytes,
-                                A.pool.base + entry * A.pool.page_stride + h * A.pool.head_stride, block_bytes, &full[s]);
+        }
+        const int l0 = in << ppt_shift;
+        const uint32_t there = (__ballot_sync(0xffffffffu, entry >= 0) >> l0) & ((1u << ppt) - 1u);
+        if (lane == 0) {
+            s_there[s] = there;
+            mbar_expect_tx(&full[s], __popc(there) * Blk::bytes(P));
+        }
+        __syncwarp();
+        if (lane >= l0 && lane < l0 + ppt && entry >= 0) {
+            const unsigned char* from = A.pool.base + entry * A.pool.page_stride + g.h * A.pool.head_stride;
+            unsigned char* to = smem + s * Cfg::kStageBytes;
+            const int at = (lane - l0) << p_shift;
+            if (P == kTile) {
+                tma_load_1d(to, from, Blk::bytes(kTile), &full[s]);
+            } else {
+                tma_load_1d(to + at * Blk::kRow, from, P * Blk::kRow, &full[s]);
+                tma_load_1d(to + kKs + at * Blk::kScl, from + P * Blk::kRow, P * Blk::kScl, &full[s]);
+                tma_load_1d(to + kV + at * Blk::kRow, from + Blk::v_codes(P), P * Blk::kRow, &full[s]);
+                tma_load_1d(to + kVs + at * Blk::kScl, from + Blk::v_codes(P) + P * Blk::kRow, P * Blk::kScl, &full[s]);
             }
-        };
-        if (!s_dead)
+        }
+    };
+    // The start of a segment, as far as it can run beside the end of the one
+    // before it: first copies, and Q's rows into the buffer of P^T.
+    auto begin = [&](const Seg& g) {
+        if (warp == 0 && !s_dead)
 #pragma unroll
             for (int s = 0; s < kS; ++s)
-                if (s < tiles) issue(s, s, s);
-
-        // ---- Q, laid out like the keys' words -------------------------------
-        if (tid < kRows) {
-            const int rho = row0 + tid, i = rho / A.G, g = rho - i * A.G;
-            const long long head = static_cast<long long>(h) * A.G + g;
-            s_q[tid] = tid < live_rows ? b * A.q_bs + i * A.q_rs + head * A.q_hs : 0;
-            s_out[tid] = rho < A.n * A.G ? (static_cast<long long>(b) * A.n + i) * A.hq + head : -1;
+                if (s < g.tiles) issue(g, s, s);
+        if (A.aligned && g.tiles > 0) {
+            for (int x = tid; x < kRows * (D / 8); x += kAtThreads) {
+                const int row = x / (D / 8), c = x % (D / 8), rho = g.row0 + row;
+                if (row < g.live_rows) {
+                    const int i = static_cast<unsigned>(rho) / static_cast<unsigned>(A.G), gq = rho - i * A.G;
+                    const uint16_t* q = A.q + g.b * A.q_bs + i * A.q_rs + (static_cast<long long>(g.h) * A.G + gq) * A.q_hs + c * 8;
+                    cp_async16(p_base + (row * (D / 8) + (c ^ (row & 7))) * 16, q);
+                }
+            }
+            cp_async_commit();
         }
+    };
+
+    Seg g = segment(lo);
+    begin(g);
+    for (;;) {
+        // ---- Q, laid out like the keys' words -------------------------------
+        const int row0 = g.row0, live_rows = g.live_rows, tiles = g.tiles, v0 = g.v0;
+        const Req rc = rq;                      // the request (rq moves on before the segment's end)
+        if (tid < kRows) {
+            const int rho = row0 + tid, i = static_cast<unsigned>(rho) / static_cast<unsigned>(A.G);
+            s_out[tid] = rho < A.n * A.G ? (static_cast<long long>(g.b) * A.n + i) * A.hq + static_cast<long long>(g.h) * A.G + rho - i * A.G : -1;
+        }
+        cp_async_wait();
         __syncthreads();
         if (tiles > 0)
             for (int x = tid; x < NT * kKW * 32; x += kAtThreads) {
                 const int l = x & 31, nt = (x >> 5) % NT, w = (x >> 5) / NT;
-                const int row = nt * 8 + (l >> 2);
+                const int row = nt * 8 + (l >> 2), c = (l & 3) * kKW + w;
                 uint32_t y[4] = {0, 0, 0, 0};
                 if (row < live_rows) {
-                    const uint16_t* q = A.q + s_q[row] + (l & 3) * (D / 4) + 8 * w;
                     if (A.aligned) {
-                        const uint4 t = *reinterpret_cast<const uint4*>(q);
-                        y[0] = t.x; y[1] = t.y; y[2] = t.z; y[3] = t.w;
+                        lds(y, p_base + (row * (D / 8) + (c ^ (row & 7))) * 16);
                     } else {
+                        const int rho = row0 + row, i = static_cast<unsigned>(rho) / static_cast<unsigned>(A.G), gq = rho - i * A.G;
+                        const uint16_t* q = A.q + g.b * A.q_bs + i * A.q_rs + (static_cast<long long>(g.h) * A.G + gq) * A.q_hs + c * 8;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) y[e] = q[2 * e] | (static_cast<uint32_t>(q[2 * e + 1]) << 16);
                     }
@@ -470,26 +529,25 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
         // ---- the tiles -------------------------------------------------------
         int s = 0, refill = kS - 1;             // this tile's stage, the one before it
         for (int k = 0; k < tiles; ++k) {
-            const int t0 = rq.real(v0 + k) * kTile;
-            const uint32_t there = fifo & 15u;
-            fifo >>= 4;
+            const int t0 = rc.real(v0 + k) * kTile;
             if (!s_dead && !mbar_wait(&full[s], (phases >> s) & 1u)) {
                 s_dead = 1;
                 atomicOr(&L.ctrl->error, SPEC_WS_ERR_WAIT);
             }
+            const uint32_t there = s_there[s];
             phases ^= 1u << s;
             const uint32_t stage = ring + s * Cfg::kStageBytes;
             const uint32_t pbuf = p_base + (k & 1) * Cfg::kP;
             // every row sees every key of most tiles
-            const bool masked = t0 + kTile > rq.ctx || there != (1u << ppt) - 1u ||
-                                (A.window > 0 && t0 + kTile > A.sinks && t0 < rq.low + A.n);
+            const bool masked = t0 + kTile > rc.ctx || there != (1u << ppt) - 1u ||
+                                (A.window > 0 && t0 + kTile > A.sinks && t0 < rc.low + A.n);
             auto tile = [&](auto is_masked) {
                 constexpr bool kMasked = decltype(is_masked)::value;
                 unsigned long long any = ~0ull;
                 if constexpr (kMasked) {
                     if (tid < kRows) {
                         unsigned long long v = 0;
-                        if (tid < live_rows) v = seen64(A, rq, b, (row0 + tid) / A.G, t0);
+                        if (tid < live_rows) v = seen64(A, rc, g.b, static_cast<unsigned>(row0 + tid) / static_cast<unsigned>(A.G), t0);
 #pragma unroll 1
                         for (int q = 0; q < ppt; ++q)
                             if (!(there >> q & 1u)) v &= ~range64(q << p_shift, (q + 1) << p_shift, 0);
@@ -504,8 +562,10 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
                 }
                 // S^T = K Q^T: this warp's 16 tokens
                 float x[NT][4];
+                [[maybe_unused]] float y[NT][4];            // one block of rows: two chains of sums, for latency
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.0f;
+                if constexpr (NT == 1) y[0][0] = y[0][1] = y[0][2] = y[0][3] = 0.0f;
                 {
                     uint32_t wa[kKW], wb[kKW];
                     lds(wa, stage + k_at);
@@ -516,7 +576,7 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             if constexpr (Cfg::kQInRegs) {
-                                mma(x[nt], a, qf[ks][nt][0], qf[ks][nt][1]);
+                                mma(ks & 1 ? y[nt] : x[nt], a, qf[ks][nt][0], qf[ks][nt][1]);
                             } else {
                                 uint32_t q2[2];
                                 lds(q2, q_base + ((ks * NT + nt) * 32 + lane) * 8);
@@ -532,6 +592,10 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
                         const uint32_t a1[4] = {codes2<2>(wa[w], sa, ca), codes2<2>(wb[w], sb, cb),
                                                 codes2<3>(wa[w], sa, ca), codes2<3>(wb[w], sb, cb)};
                         step(2 * w + 1, a1);
+                    }
+                    if constexpr (NT == 1) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[0][e] += y[0][e];
                     }
                 }
                 if constexpr (kMasked) {
@@ -613,7 +677,7 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
                     __syncthreads();
                 }
                 // every warp is past the tile before this one: its stage is free
-                if (k > 0 && k - 1 + kS < tiles && !s_dead) issue(k - 1 + kS, refill, kS - 2);
+                if (warp == 0 && k > 0 && k - 1 + kS < tiles && !s_dead) issue(g, k - 1 + kS, refill);
                 const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -621,22 +685,24 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
                     l[nt][1] += ls[nt][1];
                 }
                 // O^T += V^T P^T: this warp's rows, all tokens
+                uint32_t vscale;
+                {
+                    uint32_t s0 = lds16(stage + vs0_at), s1 = lds16(stage + vs1_at);
+                    if constexpr (kMasked) {    // what no row sees may be anything, NaN among it
+                        const uint32_t a = static_cast<uint32_t>(any >> ((lane >> 2) * 8));
+                        s0 = a >> tv0 & 1 ? s0 : 0;
+                        s1 = a >> tv1 & 1 ? s1 : 0;
+                    }
+                    vscale = s0 | s1 << 16;
+                }
 #pragma unroll
                 for (int mb = 0; mb < 4; ++mb) {
-                    const uint32_t vr = stage + at16(mb, Blk::kRow), vs = stage + at16(mb, Blk::kScl);
+                    const uint32_t vr = stage + mb * 16 * Blk::kRow;
                     // token pairs side by side: four (two) codes each
                     const uint32_t ab = __byte_perm(ldsv<D>(vr + v0_at), ldsv<D>(vr + v1_at), 0x5410);
                     const uint32_t cd = __byte_perm(ldsv<D>(vr + v0_at + 8 * Blk::kRow), ldsv<D>(vr + v1_at + 8 * Blk::kRow), 0x5410);
-                    uint32_t s0 = lds16(vs + vs0_at), s1 = lds16(vs + vs1_at);
-                    uint32_t s2 = lds16(vs + vs0_at + 8 * Blk::kScl), s3 = lds16(vs + vs1_at + 8 * Blk::kScl);
-                    if constexpr (kMasked) {    // what no row sees may be anything, NaN among it
-                        const uint32_t a = static_cast<uint32_t>(any >> (mb * 16));
-                        s0 = a >> tv0 & 1 ? s0 : 0;
-                        s1 = a >> tv1 & 1 ? s1 : 0;
-                        s2 = a >> (tv0 + 8) & 1 ? s2 : 0;
-                        s3 = a >> (tv1 + 8) & 1 ? s3 : 0;
-                    }
-                    const uint32_t sa = s0 | s1 << 16, sb = s2 | s3 << 16;
+                    const uint32_t sa = __shfl_sync(0xffffffffu, vscale, mb * 8 + c4);
+                    const uint32_t sb = __shfl_sync(0xffffffffu, vscale, mb * 8 + 4 + c4);
                     const uint32_t ca = minus1_5(sa), cb = minus1_5(sb);
                     uint32_t a[kMT][4];
                     a[0][0] = codes2<0>(ab, sa, ca);
@@ -685,33 +751,40 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
                 if (r8 == 0 && (nt & 3) == warp) s_lr[nt * 8 + 2 * c4 + e] = lr[nt >> 2][e];
             }
         __syncthreads();
-        const bool whole = v0 == 0 && v1 == tiles_u;
+        // every warp is past its last tile: the next segment may begin
+        const Seg cur = g;
+        const bool more = cur.u_from + cur.v1 < hi;
+        if (more) {
+            g = segment(cur.u_from + cur.v1);
+            begin(g);
+        }
+        const bool whole = v0 == 0 && cur.v1 == cur.tiles_u;
         // the CTA that holds the unit's first tile, and how many share it
         int c0 = cta, parts = 1;
         if (!whole) {
             auto cta_of = [&](long long x) {
-                int c = static_cast<int>(x * active / total);
+                const long long y = x * active;
+                int c = static_cast<int>((y | total) >> 32 ? y / total
+                                                           : static_cast<unsigned>(y) / static_cast<unsigned>(total));
                 while (start_of(c + 1) <= x) ++c;
                 while (start_of(c) > x) --c;
                 return c;
             };
-            c0 = v0 == 0 ? cta : cta_of(u_from);
-            parts = (v1 == tiles_u ? cta : cta_of(u_from + tiles_u - 1)) - c0 + 1;
+            c0 = v0 == 0 ? cta : cta_of(cur.u_from);
+            parts = (cur.v1 == cur.tiles_u ? cta : cta_of(cur.u_from + cur.tiles_u - 1)) - c0 + 1;
         }
         const int slot = 2 * cta + (c0 == cta ? 1 : 0);
         const int d0 = warp * (D / 4) + r8 * (D / 32);          // this lane's D/32 values of a row
-        auto emit = [&](int row, const float (&v)[2 * kMT], float mm, float sum, float rsum) {
-            const long long at = s_out[row];
-            if (at < 0) return;
-            const bool on = row < live_rows && sum != 0.0f;
-            const float f = on ? 16.0f / rsum : 0.0f;
-            uint32_t u[kMT];
-#pragma unroll
-            for (int j = 0; j < kMT; ++j) u[j] = on ? pack_bf16(v[2 * j] * f, v[2 * j + 1] * f) : 0;
-            uint16_t* to = A.out + at * D + d0;
-            if constexpr (kMT == 2) *reinterpret_cast<uint2*>(to) = make_uint2(u[0], u[1]);
-            else *reinterpret_cast<uint32_t*>(to) = u[0];
-            if (A.lse && warp == 0 && r8 == 0) A.lse[at] = on ? (mm + log2f(sum)) * kLn2 : -CUDART_INF_F;
+        // D/32 values from d on of a row, times f, into the output
+        auto emit = [&](long long at, int d, const float (&v)[2 * kMT], float f) {
+            uint16_t* to = A.out + at * D + d;
+            if constexpr (kMT == 2)
+                *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16(v[0] * f, v[1] * f), pack_bf16(v[2] * f, v[3] * f));
+            else
+                *reinterpret_cast<uint32_t*>(to) = pack_bf16(v[0] * f, v[1] * f);
+        };
+        auto emit_lse = [&](long long at, bool on, float mm, float sum) {
+            if (A.lse) A.lse[at] = on ? (mm + log2f(sum)) * kLn2 : -CUDART_INF_F;
         };
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -728,7 +801,16 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
                     v[2 * j + 1] = o[j][nt][2 + e];
                 }
                 if (whole) {
-                    emit(row, v, m[nt][e], sum, rsum);
+                    const long long at = s_out[row];
+                    const bool on = row < live_rows && sum != 0.0f;
+                    if (at >= 0) {
+                        if (!on) {              // nothing seen: whatever O^T holds there
+#pragma unroll
+                            for (int j = 0; j < 2 * kMT; ++j) v[j] = 0.0f;
+                        }
+                        emit(at, d0, v, on ? 16.0f / rsum : 0.0f);
+                        if (warp == 0 && r8 == 0) emit_lse(at, on, m[nt][e], sum);
+                    }
                 } else {
                     const long long at = static_cast<long long>(slot) * kRows + row;
                     if constexpr (kMT == 2)
@@ -750,34 +832,54 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
             __syncthreads();
             if (s_last) {
                 __threadfence();
-#pragma unroll 1
-                for (int ne = 0; ne < 2 * NT; ++ne) {
-                    const int row = (ne >> 1) * 8 + 2 * c4 + (ne & 1);
-                    auto place = [&](int c) { return (2ll * (c0 + c) + (c == 0 ? 1 : 0)) * kRows + row; };
-                    float mm = kNoMax;
+                auto place = [&](int c, int row) { return (2ll * (c0 + c) + (c == 0 ? 1 : 0)) * kRows + row; };
+                // first each row's maximum and sums, then the values, D/32 a thread
+                if (tid < kRows) {
+                    float mm = kNoMax, sum = 0.0f, rsum = 0.0f;
 #pragma unroll 4
-                    for (int c = 0; c < parts; ++c) mm = fmaxf(mm, __ldcg(L.ml + place(c) * 4));
-                    float v[2 * kMT] = {}, sum = 0.0f, rsum = 0.0f;
+                    for (int c = 0; c < parts; ++c) mm = fmaxf(mm, __ldcg(L.ml + place(c, tid) * 4));
 #pragma unroll 4
                     for (int c = 0; c < parts; ++c) {
-                        const float4 ml = __ldcg(reinterpret_cast<const float4*>(L.ml) + place(c));
+                        const float4 ml = __ldcg(reinterpret_cast<const float4*>(L.ml) + place(c, tid));
                         const float f = exp2_fast(ml.x - mm);
                         sum += f * ml.y;
                         rsum += f * ml.z;
+                    }
+                    const bool on = tid < live_rows && sum != 0.0f;
+                    s_max[0][tid] = mm;
+                    s_max[1][tid] = on ? 16.0f / rsum : 0.0f;
+                    s_max[2][tid] = on ? 1.0f : 0.0f;
+                    if (s_out[tid] >= 0) emit_lse(s_out[tid], on, mm, sum);
+                }
+                __syncthreads();
+                for (int x = tid; x < kRows * 32; x += kAtThreads) {
+                    const int row = x >> 5, d = (x & 31) * (D / 32);
+                    const long long at = s_out[row];
+                    if (at < 0) continue;
+                    const float mm = s_max[0][row];
+                    float v[2 * kMT] = {};
+#pragma unroll 4
+                    for (int c = 0; c < parts; ++c) {
+                        const long long from = place(c, row);
+                        const float f = exp2_fast(__ldcg(L.ml + from * 4) - mm);
                         if constexpr (kMT == 2) {
-                            const float4 z = __ldcg(reinterpret_cast<const float4*>(L.part + place(c) * D + d0));
+                            const float4 z = __ldcg(reinterpret_cast<const float4*>(L.part + from * D + d));
                             v[0] += f * z.x; v[1] += f * z.y; v[2] += f * z.z; v[3] += f * z.w;
                         } else {
-                            const float2 z = __ldcg(reinterpret_cast<const float2*>(L.part + place(c) * D + d0));
+                            const float2 z = __ldcg(reinterpret_cast<const float2*>(L.part + from * D + d));
                             v[0] += f * z.x; v[1] += f * z.y;
                         }
                     }
-                    emit(row, v, mm, sum, rsum);
+                    if (s_max[2][row] == 0.0f) {
+#pragma unroll
+                        for (int j = 0; j < 2 * kMT; ++j) v[j] = 0.0f;
+                    }
+                    emit(at, d, v, s_max[1][row]);
                 }
             }
         }
+        if (!more) break;
         __syncthreads();                        // shared memory is written again
-        pos = u_from + v1;
     }
 }
 
