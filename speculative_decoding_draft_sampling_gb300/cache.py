@@ -28,7 +28,7 @@ from typing import Optional
 
 import torch
 
-from . import SpecError, _check, _cuda, _dev, _load, _p, _stream
+from . import SpecError, _check, _cuda, _load
 
 ST_BAD_PAGE, ST_NO_PAGE = 128, 256
 
@@ -70,81 +70,104 @@ def cache_block_bytes(head_dim: int, page_size: int) -> int:
     return n
 
 
-def _ints(t, name: str, shape, contiguous: bool = True):
-    _cuda(t, name, torch.int32)
-    if tuple(t.shape) != tuple(shape) or (contiguous and not t.is_contiguous()):
-        raise SpecError(f"{name} must be a contiguous {list(shape)} int32 tensor")
-    return t
+_i32, _bf16, _u8 = torch.int32, torch.bfloat16, torch.uint8
 
 
-def _opt_ints(t, name: str, shape):
-    return None if t is None else _ints(t, name, shape)
+# A decoding step makes these calls for every layer, so the checks below look at
+# each tensor once and say what is wrong only where something is.
+def _ints(t, name: str, *shape) -> int:
+    """The address of a contiguous int32 tensor of this shape."""
+    if isinstance(t, torch.Tensor) and t.dtype is _i32 and t.shape == shape and t.is_contiguous() \
+            and (t.is_cuda or t.is_pinned()):
+        return t.data_ptr()
+    _cuda(t, name, _i32)
+    raise SpecError(f"{name} must be a contiguous {list(shape)} int32 tensor")
+
+
+def _opt(t, name: str, *shape):
+    return None if t is None else _ints(t, name, *shape)
 
 
 def _pool(pool, dims: int, head_dim: int):
     """(page_size, kv_heads, num_pages) of a pool of `dims` dimensions."""
-    if not isinstance(pool, torch.Tensor) or not pool.is_cuda or pool.dtype != torch.uint8 or pool.dim() != dims \
+    if not isinstance(pool, torch.Tensor) or not pool.is_cuda or pool.dtype is not _u8 or pool.dim() != dims \
             or pool.stride(-1) != 1:
         raise SpecError("pool must be a uint8 CUDA tensor "
                         + ("[pages, kv_heads, block]" if dims == 3 else "[layers, pages, kv_heads, block]")
                         + " with unit element stride")
-    page = pool.shape[-1] * 8 // (9 * head_dim)
-    if page not in (16, 32, 64) or page * head_dim * 9 // 8 != pool.shape[-1]:
-        raise SpecError(f"a block of {pool.shape[-1]} bytes is no page of head_dim {head_dim}")
-    return page, pool.shape[-2], pool.shape[-3]
+    pages, heads, block = pool.shape[-3:]
+    page = block * 8 // (9 * head_dim)
+    if page not in (16, 32, 64) or page * head_dim * 9 != block * 8:
+        raise SpecError(f"a block of {block} bytes is no page of head_dim {head_dim}")
+    return page, heads, pages
 
 
 def _table(page_table, B: Optional[int] = None):
-    _cuda(page_table, "page_table", torch.int32)
-    if page_table.dim() != 2 or page_table.stride(1) != 1 or (B is not None and page_table.shape[0] != B):
-        raise SpecError("page_table must be [B, M] int32 with unit element stride")
-    return page_table.shape
+    """B, M, the row stride and the address of a page table."""
+    if isinstance(page_table, torch.Tensor) and page_table.dtype is _i32 and page_table.dim() == 2 \
+            and (page_table.is_cuda or page_table.is_pinned()):
+        (rows, width), (stride, unit) = page_table.shape, page_table.stride()
+        if unit == 1 and (B is None or rows == B):
+            return rows, width, stride, page_table.data_ptr()
+    _cuda(page_table, "page_table", _i32)
+    raise SpecError("page_table must be [B, M] int32 with unit element stride")
+
+
+def _handle(stream, device: torch.device) -> int:
+    """The stream's handle: of the one given, else of the device's current one."""
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
 def cache_append(k, v, pool, page_table, start, count=None, *, status=None, stream=None) -> None:
     """Write k, v [B, n, kv_heads, D] bf16 (any strides, unit element stride)
     into the cache in 4 bits: row (b, i), i < count[b] (default n), at position
     start[b] + i.  Groups of 32 values share a scale."""
-    L = _lib()
-    _cuda(k, "k", torch.bfloat16)
-    _cuda(v, "v", torch.bfloat16)
-    if k.dim() != 4 or v.shape != k.shape or k.stride(3) != 1 or v.stride(3) != 1:
+    if not (isinstance(k, torch.Tensor) and isinstance(v, torch.Tensor) and k.dtype is _bf16 and v.dtype is _bf16
+            and (k.is_cuda or k.is_pinned()) and (v.is_cuda or v.is_pinned())):
+        _cuda(k, "k", _bf16)
+        _cuda(v, "v", _bf16)
+    shape = k.shape
+    if len(shape) != 4 or v.shape != shape:
         raise SpecError("k and v must be [B, n, kv_heads, D] with unit element stride")
-    B, n, H, D = k.shape
+    B, n, H, D = shape
+    kb, kr, kh, k1 = k.stride()
+    vb, vr, vh, v1 = v.stride()
+    if k1 != 1 or v1 != 1:
+        raise SpecError("k and v must be [B, n, kv_heads, D] with unit element stride")
     page, heads, pages = _pool(pool, 3, D)
     if heads != H:
         raise SpecError(f"the pool has {heads} kv heads, k and v {H}")
-    M = _table(page_table, B)[1]
-    _check(L.spec_cache_append(_p(k), k.stride(0), k.stride(1), k.stride(2),
-                               _p(v), v.stride(0), v.stride(1), v.stride(2),
-                               _p(pool), pool.stride(0), pool.stride(1), pages,
-                               _p(page_table), page_table.stride(0), M,
-                               _p(_ints(start, "start", (B,))), _p(_opt_ints(count, "count", (B,))),
-                               B, n, H, D, page, _p(_opt_ints(status, "status", (B,))), _stream(stream)),
-           "spec_cache_append")
+    _, M, ts, tp = _table(page_table, B)
+    ps, hs, _ = pool.stride()
+    rc = _lib().spec_cache_append(k.data_ptr(), kb, kr, kh, v.data_ptr(), vb, vr, vh, pool.data_ptr(), ps, hs, pages,
+                                  tp, ts, M, _ints(start, "start", B), _opt(count, "count", B), B, n, H, D, page,
+                                  _opt(status, "status", B), _handle(stream, pool.device))
+    if rc:
+        _check(rc, "spec_cache_append")
 
 
 def cache_read(pool, page_table, start, n: int, head_dim: int, count=None, *, k=None, v=None, status=None,
                stream=None):
     """Rows of the cache as bf16 values, exactly what the codes stand for:
     (k, v), each [B, n, kv_heads, D]; rows i >= count[b] are 0."""
-    L = _lib()
     page, H, pages = _pool(pool, 3, head_dim)
-    B, M = _table(page_table)
-    shape = (B, int(n), H, int(head_dim))
-    out = []
-    for t, name in ((k, "k"), (v, "v")):
-        if t is None:
-            t = torch.empty(shape, dtype=torch.bfloat16, device=pool.device)
-        elif _cuda(t, name, torch.bfloat16).shape != shape or not t.is_contiguous():
-            raise SpecError(f"{name} must be a contiguous {list(shape)} bf16 tensor")
-        out.append(t)
-    _check(L.spec_cache_read(_p(pool), pool.stride(0), pool.stride(1), pages,
-                             _p(page_table), page_table.stride(0), M,
-                             _p(_ints(start, "start", (B,))), _p(_opt_ints(count, "count", (B,))),
-                             B, int(n), H, int(head_dim), page, _p(out[0]), _p(out[1]),
-                             _p(_opt_ints(status, "status", (B,))), _stream(stream)), "spec_cache_read")
-    return out[0], out[1]
+    B, M, ts, tp = _table(page_table)
+    shape = (B, n, H, head_dim)
+    if k is None:
+        k = torch.empty(shape, dtype=_bf16, device=pool.device)
+    elif _cuda(k, "k", _bf16).shape != shape or not k.is_contiguous():
+        raise SpecError(f"k must be a contiguous {list(shape)} bf16 tensor")
+    if v is None:
+        v = torch.empty(shape, dtype=_bf16, device=pool.device)
+    elif _cuda(v, "v", _bf16).shape != shape or not v.is_contiguous():
+        raise SpecError(f"v must be a contiguous {list(shape)} bf16 tensor")
+    ps, hs, _ = pool.stride()
+    rc = _lib().spec_cache_read(pool.data_ptr(), ps, hs, pages, tp, ts, M, _ints(start, "start", B),
+                                _opt(count, "count", B), B, n, H, head_dim, page, k.data_ptr(), v.data_ptr(),
+                                _opt(status, "status", B), _handle(stream, pool.device))
+    if rc:
+        _check(rc, "spec_cache_read")
+    return k, v
 
 
 @dataclass
@@ -157,10 +180,9 @@ class CacheAttention:
 _attend_ws: dict = {}
 
 
-def _attend_workspace(nbytes: int, device: torch.device, stream) -> torch.Tensor:
+def _attend_workspace(nbytes: int, device: torch.device, handle: int, stream) -> torch.Tensor:
     """cache_attend's workspace, one per device and stream: its control words
     start at zero and every call leaves them so."""
-    handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
     key = (device.index, handle)
     buf = _attend_ws.get(key)
     if buf is None or buf.numel() < nbytes:
@@ -188,36 +210,44 @@ def cache_attend(q, pool, page_table, ctx_len, num_rows=None, *, anc_mask=None, 
     lse -inf; lse (natural log) is written when given or asked for.  A ws of
     one's own starts zeroed and serves one stream."""
     L = _lib()
-    _cuda(q, "q", torch.bfloat16)
-    if q.dim() != 4 or q.stride(3) != 1:
+    if not (isinstance(q, torch.Tensor) and q.dtype is _bf16 and q.dim() == 4 and (q.is_cuda or q.is_pinned())):
+        _cuda(q, "q", _bf16)
         raise SpecError("q must be [B, n, q_heads, D] with unit element stride")
-    B, n, hq, D = q.shape
+    shape = q.shape
+    B, n, hq, D = shape
+    qb, qr, qh, q1 = q.stride()
+    if q1 != 1:
+        raise SpecError("q must be [B, n, q_heads, D] with unit element stride")
     page, H, pages = _pool(pool, 3, D)
-    M = _table(page_table, B)[1]
-    dev = _dev(q)
+    _, M, ts, tp = _table(page_table, B)
+    dev = pool.device
     if anc_mask is not None:
         _cuda(anc_mask, "anc_mask", torch.int64)
-        if tuple(anc_mask.shape) != (B, n, (n + 63) // 64) or not anc_mask.is_contiguous():
+        if anc_mask.shape != (B, n, (n + 63) // 64) or not anc_mask.is_contiguous():
             raise SpecError("anc_mask must be a contiguous [B, n, ceil(n/64)] int64 tensor")
     if out is None:
-        out = torch.empty((B, n, hq, D), dtype=torch.bfloat16, device=dev)
-    elif _cuda(out, "out", torch.bfloat16).shape != q.shape or not out.is_contiguous():
+        out = torch.empty(shape, dtype=_bf16, device=dev)
+    elif _cuda(out, "out", _bf16).shape != shape or not out.is_contiguous():
         raise SpecError("out must be a contiguous tensor of q's shape, bf16")
-    if lse is None and want_lse:
-        lse = torch.empty((B, n, hq), dtype=torch.float32, device=dev)
-    elif lse is not None and (_cuda(lse, "lse", torch.float32).shape != (B, n, hq) or not lse.is_contiguous()):
-        raise SpecError("lse must be a contiguous [B, n, q_heads] float32 tensor")
-    need = L.spec_cache_attend_workspace_size(B, n, hq, H, D)
-    if ws is None and need > 0:
-        ws = _attend_workspace(need, dev, stream)
-    _check(L.spec_cache_attend(_p(q), q.stride(0), q.stride(1), q.stride(2),
-                               _p(pool), pool.stride(0), pool.stride(1), pages,
-                               _p(page_table), page_table.stride(0), M,
-                               _p(_ints(ctx_len, "ctx_len", (B,))), _p(_opt_ints(num_rows, "num_rows", (B,))),
-                               _p(anc_mask), _p(_opt_ints(depth, "depth", (B, n))), int(window), int(sinks),
-                               1.0 / math.sqrt(D) if scale is None else float(scale),
-                               B, n, hq, H, D, page, _p(out), _p(lse), _p(_opt_ints(status, "status", (B,))),
-                               _p(ws), 0 if ws is None else ws.numel(), _stream(stream)), "spec_cache_attend")
+    if lse is not None:
+        if _cuda(lse, "lse", torch.float32).shape != shape[:3] or not lse.is_contiguous():
+            raise SpecError("lse must be a contiguous [B, n, q_heads] float32 tensor")
+    elif want_lse:
+        lse = torch.empty(shape[:3], dtype=torch.float32, device=dev)
+    handle = _handle(stream, dev)
+    if ws is None:
+        need = L.spec_cache_attend_workspace_size(B, n, hq, H, D)
+        ws = _attend_workspace(need, dev, handle, stream) if need else None
+    ps, hs, _ = pool.stride()
+    rc = L.spec_cache_attend(q.data_ptr(), qb, qr, qh, pool.data_ptr(), ps, hs, pages, tp, ts, M,
+                             _ints(ctx_len, "ctx_len", B), _opt(num_rows, "num_rows", B),
+                             None if anc_mask is None else anc_mask.data_ptr(), _opt(depth, "depth", B, n),
+                             window, sinks, 1.0 / math.sqrt(D) if scale is None else scale,
+                             B, n, hq, H, D, page, out.data_ptr(), None if lse is None else lse.data_ptr(),
+                             _opt(status, "status", B), None if ws is None else ws.data_ptr(),
+                             0 if ws is None else ws.numel(), handle)
+    if rc:
+        _check(rc, "spec_cache_attend")
     return CacheAttention(out, lse, ws)
 
 
@@ -226,18 +256,18 @@ def cache_compact(pool, page_table, ctx_len, path_nodes, num_accepted, head_dim:
     """Keep an accepted path's rows: position ctx_len[b] + path_nodes[b, j]
     moves to ctx_len[b] + j, j = 0..num_accepted[b], in every layer of pool
     [layers, pages, kv_heads, block].  In place."""
-    L = _lib()
     page, H, pages = _pool(pool, 4, head_dim)
-    B, M = _table(page_table)
-    _cuda(path_nodes, "path_nodes", torch.int32)
-    if path_nodes.dim() != 2 or path_nodes.shape[0] != B or not path_nodes.is_contiguous():
+    B, M, ts, tp = _table(page_table)
+    if not isinstance(path_nodes, torch.Tensor) or path_nodes.dim() != 2:
         raise SpecError("path_nodes must be a contiguous [B, path_width] int32 tensor")
-    _check(L.spec_cache_compact(_p(pool), pool.shape[0], pool.stride(0), pool.stride(1), pool.stride(2), pages,
-                                _p(page_table), page_table.stride(0), M, _p(_ints(ctx_len, "ctx_len", (B,))),
-                                _p(path_nodes), path_nodes.shape[1],
-                                _p(_ints(num_accepted, "num_accepted", (B,))),
-                                B, H, int(head_dim), page, _p(_opt_ints(status, "status", (B,))), _stream(stream)),
-           "spec_cache_compact")
+    width = path_nodes.shape[1]
+    ls, ps, hs, _ = pool.stride()
+    rc = _lib().spec_cache_compact(pool.data_ptr(), pool.shape[0], ls, ps, hs, pages, tp, ts, M,
+                                   _ints(ctx_len, "ctx_len", B), _ints(path_nodes, "path_nodes", B, width), width,
+                                   _ints(num_accepted, "num_accepted", B), B, H, head_dim, page,
+                                   _opt(status, "status", B), _handle(stream, pool.device))
+    if rc:
+        _check(rc, "spec_cache_compact")
 
 
 # ---------------------------------------------------------------------------
@@ -262,14 +292,10 @@ def page_state(requests: int, max_pages: int, num_pages: int, device) -> PageSta
 
 
 def _pages(s: PageState):
-    R, M = _table(s.page_table)
+    R, M, ts, tp = _table(s.page_table)
     n = s.ref.shape[0]
-    _ints(s.num_held, "num_held", (R,))
-    _ints(s.ref, "ref", (n,))
-    _ints(s.free_list, "free_list", (n,))
-    _ints(s.num_free, "num_free", (1,))
-    return R, (_p(s.page_table), s.page_table.stride(0), M, _p(s.num_held), _p(s.ref), _p(s.free_list),
-               _p(s.num_free), n)
+    return R, (tp, ts, M, _ints(s.num_held, "num_held", R), _ints(s.ref, "ref", n),
+               _ints(s.free_list, "free_list", n), _ints(s.num_free, "num_free", 1), n)
 
 
 def cache_reserve(pages: PageState, length, page_size: int, *, status=None, stream=None) -> None:
@@ -277,16 +303,20 @@ def cache_reserve(pages: PageState, length, page_size: int, *, status=None, stre
     of the stack, requests in order; one that they do not suffice for gets none
     (ST_NO_PAGE)."""
     R, args = _pages(pages)
-    _check(_lib().spec_cache_reserve(*args, _p(_ints(length, "length", (R,))), R, int(page_size),
-                                     _p(_opt_ints(status, "status", (R,))), _stream(stream)), "spec_cache_reserve")
+    rc = _lib().spec_cache_reserve(*args, _ints(length, "length", R), R, page_size, _opt(status, "status", R),
+                                   _handle(stream, pages.ref.device))
+    if rc:
+        _check(rc, "spec_cache_reserve")
 
 
 def cache_release(pages: PageState, length, page_size: int, *, status=None, stream=None) -> None:
     """Each request keeps the pages of length[r] tokens (0: none); pages that
     nothing holds any more are free."""
     R, args = _pages(pages)
-    _check(_lib().spec_cache_release(*args, _p(_ints(length, "length", (R,))), R, int(page_size),
-                                     _p(_opt_ints(status, "status", (R,))), _stream(stream)), "spec_cache_release")
+    rc = _lib().spec_cache_release(*args, _ints(length, "length", R), R, page_size, _opt(status, "status", R),
+                                   _handle(stream, pages.ref.device))
+    if rc:
+        _check(rc, "spec_cache_release")
 
 
 def cache_fork(pool, pages: PageState, src, dst, length, head_dim: int, *, new_page=None, status=None, stream=None):
@@ -294,17 +324,18 @@ def cache_fork(pool, pages: PageState, src, dst, length, head_dim: int, *, new_p
     length[src[f]] tokens: full pages are shared, the last partial one is copied
     in every layer of pool [layers, pages, kv_heads, block].  Returns new_page
     [F]: the page of its own that each got, or -1."""
-    L = _lib()
     page, H, count = _pool(pool, 4, head_dim)
     R, args = _pages(pages)
-    if pages.ref.shape[0] != count:
-        raise SpecError(f"the state has {pages.ref.shape[0]} pages, the pool {count}")
+    if args[-1] != count:
+        raise SpecError(f"the state has {args[-1]} pages, the pool {count}")
     F = src.shape[0]
     if new_page is None:
-        new_page = torch.empty(F, dtype=torch.int32, device=pool.device)
-    _check(L.spec_cache_fork(_p(pool), pool.shape[0], pool.stride(0), pool.stride(1), pool.stride(2), *args,
-                             _p(_ints(src, "src", (F,))), _p(_ints(dst, "dst", (F,))),
-                             _p(_ints(length, "length", (R,))), R, F, H, int(head_dim), page,
-                             _p(_ints(new_page, "new_page", (F,))), _p(_opt_ints(status, "status", (F,))),
-                             _stream(stream)), "spec_cache_fork")
+        new_page = torch.empty(F, dtype=_i32, device=pool.device)
+    ls, ps, hs, _ = pool.stride()
+    rc = _lib().spec_cache_fork(pool.data_ptr(), pool.shape[0], ls, ps, hs, *args, _ints(src, "src", F),
+                                _ints(dst, "dst", F), _ints(length, "length", R), R, F, H, head_dim, page,
+                                _ints(new_page, "new_page", F), _opt(status, "status", F),
+                                _handle(stream, pool.device))
+    if rc:
+        _check(rc, "spec_cache_fork")
     return new_page

@@ -30,6 +30,7 @@
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "../../include/spec_cache.h"
@@ -888,11 +889,26 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
     }
 }
 
-int sm_count() {
-    int d = 0, v = 0;
-    if (cudaGetDevice(&d) != cudaSuccess || cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, d) != cudaSuccess) {
+int device() {
+    int d = 0;
+    if (cudaGetDevice(&d) != cudaSuccess) {
         cudaGetLastError();
-        return 152;
+        return 64;                              // no device: sizes are asked for on a GB300's behalf
+    }
+    return d;
+}
+
+int sm_count() {
+    static std::atomic<int> known[64];
+    const int d = device();
+    if (d >= 64) return 152;
+    int v = known[d].load(std::memory_order_relaxed);
+    if (v == 0) {
+        if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, d) != cudaSuccess) {
+            cudaGetLastError();
+            return 152;
+        }
+        known[d].store(v, std::memory_order_relaxed);
     }
     return v;
 }
@@ -938,9 +954,15 @@ cudaError_t attend(const CacheAttendArgs& A, cudaStream_t st) {
     L.ctrl = reinterpret_cast<AttendCtrl*>(ws);
     L.ml = reinterpret_cast<float*>(ws + y.ml);
     L.part = reinterpret_cast<float*>(ws + y.part);
-    const cudaError_t e = cudaFuncSetAttribute(cache_attend_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               Cfg::kSmem);
-    if (e != cudaSuccess) return e;
+    // the kernel's shared memory is set once a device
+    static std::atomic<unsigned long long> ready{0};
+    const int dev = device();
+    if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+        const cudaError_t e = cudaFuncSetAttribute(cache_attend_kernel<D, NT>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
     cache_attend_kernel<D, NT><<<grid, kAtThreads, Cfg::kSmem, st>>>(A, L);
     return cudaGetLastError();
 }
