@@ -8,11 +8,17 @@
 // Quantisation of a group of 32 bf16 values x: scale s = rn5(max|x| / 7),
 // where rn5 rounds to five significant bits, code = 8 + rn(x / s), both ties
 // to even.  It is exact to the definition in real numbers although it works
-// in fp32 and multiplies by 1/s: x has 8 significant bits and s five, so x/s
-// is either exactly k + 1/2 or at least 2^-4/31 away from it, and the product
-// x * (1/s) is off by at most 7.3 * 2^-22.  Rounding the product to a multiple
-// of 2^-13 first (one fused multiply-add with 1.5 * 2^10) turns the exact ties
-// back into ties and moves nothing else across a half.
+// in fp32 and multiplies by 1/7 and 1/s: x has 8 significant bits and s five,
+// so x/s is either exactly k + 1/2 or at least 2^-4/31 away from it, and the
+// product x * (1/s) is off by less than 2^-18.  Rounding the product to a
+// multiple of 2^-13 first (one fused multiply-add with 1.5 * 2^10) turns the
+// exact ties back into ties and moves nothing else across a half; one more add
+// rounds to the integer.  Likewise max|x| / 7 is a five-bit tie or at least
+// 1/(7 * 64) of it away from one, and is rounded to 13 bits first.
+//
+// Append and read move 4 bytes of codes or 16 of values a thread with several
+// heads in flight.  Both are bound by HBM on prompts: 8 prompts of 8192 tokens,
+// 8 heads of 128 (268 MB of bf16, 75 MB of cache).
 #include <cuda_bf16.h>
 
 #include "../../include/spec_cache.h"
@@ -37,17 +43,17 @@ __device__ __forceinline__ uint4 load8(const uint16_t* p) {
     }
 }
 
-// five significant bits, ties to even; 0 below 2^-120
-__device__ __forceinline__ float round5(float x) {
-    uint32_t u = __float_as_uint(x);
+// max|x| / 7 to five significant bits, ties to even; 0 below 2^-120
+__device__ __forceinline__ float scale_of(float top) {
+    uint32_t u = __float_as_uint(__fmul_rn(top, 1.0f / 7.0f));
+    u = (u + 0x400u) & ~0x7FFu;                             // 13 bits: what 1/7 lost
     u = (u + 0x3FFFFu + ((u >> 19) & 1u)) & ~0x7FFFFu;
     return u < 0x03800000u ? 0.0f : __uint_as_float(u);
 }
 
-// code of x under a scale of reciprocal r
+// an integer whose low four bits are the code of x under a scale of reciprocal r
 __device__ __forceinline__ uint32_t code_of(float x, float r) {
-    const float t = __fadd_rn(__fmaf_rn(x, r, 1536.0f), -1536.0f);   // a multiple of 2^-13
-    return __float_as_uint(__fadd_rn(t, 12582912.0f + 8.0f)) & 15u;
+    return __float_as_uint(__fadd_rn(__fmaf_rn(x, r, 1536.0f), 12582912.0f + 8.0f - 1536.0f));
 }
 
 // Quantises a thread's eight values (four neighbouring lanes share a group, the
@@ -57,22 +63,24 @@ __device__ __forceinline__ uint32_t quantise8(uint4 x, uint32_t& scale, bool& ba
     uint32_t w[4] = {x.x, x.y, x.z, x.w};
     uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
                           __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
     m = max(m & 0xffffu, m >> 16);
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
     if (__any_sync(0xffffffffu, m >= 0x7f80u)) {
         // a NaN or an infinity in the warp: the maximum is over finite values,
         // NaN becomes 0 and an infinity the largest code
         uint32_t f = 0;
+        bool mine = false;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const uint32_t h = (w[i >> 1] >> (16 * (i & 1))) & 0x7fffu;
             if (h < 0x7f80u) f = max(f, h);
+            else mine = true;
         }
         f = max(f, __shfl_xor_sync(0xffffffffu, f, 1));
         f = max(f, __shfl_xor_sync(0xffffffffu, f, 2));
+        bad |= mine;
         if (m >= 0x7f80u) {
-            bad = true;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int sh = 16 * (i & 1);
@@ -85,128 +93,177 @@ __device__ __forceinline__ uint32_t quantise8(uint4 x, uint32_t& scale, bool& ba
             m = f;
         }
     }
-    const float s = round5(__fdiv_rn(__uint_as_float(m << 16), 7.0f));
+    const float s = scale_of(__uint_as_float(m << 16));
     scale = __float_as_uint(s) >> 16;
-    const float r = s > 0.0f ? __frcp_rn(s) : 0.0f;
-    uint32_t out = 0;
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    if (s == 0.0f) r = 0.0f;
+    uint32_t two[4];                                        // low byte: the codes of two neighbours
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        two[i] = code_of(__uint_as_float(w[i] & 0xffff0000u), r) * 16u + code_of(__uint_as_float(w[i] << 16), r);
+    return __byte_perm(__byte_perm(two[0], two[1], 0x0040), __byte_perm(two[2], two[3], 0x0040), 0x5410);
+}
+
+// How the rows are dealt out: blockIdx.x takes 8 (D = 128) or 16 tokens,
+// blockIdx.y a request, blockIdx.z a range of heads; D/8 threads take K or V of
+// one token and go through the heads, four at a time.
+template <int D>
+struct RowPlace {
+    static constexpr int kT = D / 8;                        // threads a row
+    static constexpr int kTokens = kRowThreads / kT / 2;
+    int i, c;
+    bool isv;
+    __device__ __forceinline__ RowPlace() {
+        const int group = threadIdx.x / kT;
+        c = threadIdx.x % kT;
+        isv = group & 1;
+        i = blockIdx.x * kTokens + group / 2;
+    }
+};
+
+constexpr int kFly = 4;                                     // heads in flight
+
+// Every thread of a warp takes part in the shuffles, live or not.
+template <int D, bool kAligned>
+__global__ void __launch_bounds__(kRowThreads) cache_append_kernel(const CacheRowsArgs A, int heads_per) {
+    using Blk = CacheBlock<D>;
+    const RowPlace<D> at;
+    const int c = at.c, P = A.pool.P;
+    const int h0 = blockIdx.z * heads_per, h1 = min(h0 + heads_per, A.pool.heads);
+    for (int b = blockIdx.y; b < A.B; b += gridDim.y) {
+        const bool live = at.i < (A.count ? min(A.count[b], A.n) : A.n);
+        int page = -1;
+        long long pos = 0;
+        if (live) {
+            pos = static_cast<long long>(A.start[b]) + at.i;
+            page = cache_page(A.tab, A.pool.num_pages, A.pool.p_shift, b, pos);
+        }
+        const uint16_t* src = at.isv ? A.v + b * A.v_bs + at.i * A.v_rs + c * 8 : A.k + b * A.k_bs + at.i * A.k_rs + c * 8;
+        const long long hs = at.isv ? A.v_hs : A.k_hs;
+        const int slot = static_cast<int>(pos & (P - 1));
+        unsigned char* blk = A.pool.base + page * A.pool.page_stride + (at.isv ? Blk::v_codes(P) : 0);
+        bool bad = false;
+        for (int h = h0; h < h1; h += kFly) {
+            uint4 x[kFly];
+#pragma unroll
+            for (int q = 0; q < kFly; ++q) {
+                x[q] = make_uint4(0, 0, 0, 0);
+                if (live && h + q < h1) x[q] = load8<kAligned>(src + (h + q) * hs);
+            }
+#pragma unroll
+            for (int q = 0; q < kFly; ++q) {
+                if (h + q >= h1) break;
+                uint32_t scale;
+                const uint32_t codes = quantise8(x[q], scale, bad);
+                if (page >= 0) {
+                    unsigned char* to = blk + (h + q) * A.pool.head_stride;
+                    reinterpret_cast<uint32_t*>(to + slot * Blk::kRow)[c] = codes;
+                    if ((c & 3) == 0)
+                        reinterpret_cast<uint16_t*>(to + P * Blk::kRow + slot * Blk::kScl)[c >> 2] = static_cast<uint16_t>(scale);
+                }
+            }
+        }
+        if (A.status && live && (bad || page < 0))
+            atomicOr(A.status + b, (bad ? SPEC_ST_BAD_ROW : 0) | (page < 0 ? SPEC_ST_BAD_PAGE : 0));
+    }
+}
+
+// Eight codes under scale s as bf16, in order: two codes 16 bits apart become
+// 1 + code/16, then (code - 8)/16 * s by one exact fused multiply-add with
+// (s, -1.5 s), and 16 times that (16 s itself may be out of range).
+__device__ __forceinline__ uint4 values8(uint32_t w, uint32_t s2, uint32_t c2) {
+    uint32_t v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        out |= code_of(__uint_as_float(w[i] << 16), r) << (8 * i);
-        out |= code_of(__uint_as_float(w[i] & 0xffff0000u), r) << (8 * i + 4);
+        const uint32_t t = ((i == 0 ? w << 3 : w >> (4 * i - 3)) & 0x00780078u) | 0x3F803F80u;
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(v[i]) : "r"(t), "r"(s2), "r"(c2));
+        asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(v[i]) : "r"(0x41804180u));
     }
-    return out;
-}
-
-// D/8 threads quantise a row; rows go K heads, V heads of a token, token by
-// token.  Every thread of a warp takes part in the shuffles, live or not.
-template <int D, bool kAligned>
-__global__ void __launch_bounds__(kRowThreads) cache_append_kernel(const CacheRowsArgs A) {
-    constexpr int kT = D / 8;                               // threads a row
-    const int H = A.pool.heads;
-    const long long item = (static_cast<long long>(blockIdx.x) * kRowThreads + threadIdx.x) / kT;
-    const int c = threadIdx.x % kT;
-    const long long tok = item / (2 * H);                   // b * n + i
-    const int hk = static_cast<int>(item % (2 * H));
-    const bool isv = hk >= H;
-    const int h = isv ? hk - H : hk;
-    const int b = static_cast<int>(tok / A.n), i = static_cast<int>(tok % A.n);
-    const bool live = b < A.B && i < (A.count ? A.count[b] : A.n);
-    uint4 x = make_uint4(0, 0, 0, 0);
-    int page = -1;
-    long long pos = 0;
-    if (live) {
-        pos = static_cast<long long>(A.start[b]) + i;
-        page = cache_page(A.tab, A.pool.num_pages, A.pool.p_shift, b, pos);
-        const uint16_t* src = isv ? A.v + b * A.v_bs + i * A.v_rs + h * A.v_hs
-                                  : A.k + b * A.k_bs + i * A.k_rs + h * A.k_hs;
-        x = load8<kAligned>(src + c * 8);
-    }
-    bool bad = false;
-    uint32_t scale;
-    const uint32_t codes = quantise8(x, scale, bad);
-    if (!live) return;
-    if (A.status && (bad || page < 0))
-        atomicOr(A.status + b, (bad ? SPEC_ST_BAD_ROW : 0) | (page < 0 ? SPEC_ST_BAD_PAGE : 0));
-    if (page < 0) return;
-    const int P = A.pool.P, slot = static_cast<int>(pos & (P - 1));
-    unsigned char* blk = A.pool.base + page * A.pool.page_stride + h * A.pool.head_stride +
-                         (isv ? CacheBlock<D>::v_codes(P) : 0);
-    reinterpret_cast<uint32_t*>(blk + slot * CacheBlock<D>::kRow)[c] = codes;
-    if ((c & 3) == 0)
-        reinterpret_cast<uint16_t*>(blk + P * CacheBlock<D>::kRow + slot * CacheBlock<D>::kScl)[c >> 2] =
-            static_cast<uint16_t>(scale);
-}
-
-// (code - 8) * scale of two neighbouring codes, as bf16 bits
-__device__ __forceinline__ uint32_t values2(uint32_t two, float s) {
-    const float lo = (static_cast<float>(two & 15u) - 8.0f) * s;
-    const float hi = (static_cast<float>((two >> 4) & 15u) - 8.0f) * s;
-    return (__float_as_uint(lo) >> 16) | (__float_as_uint(hi) & 0xffff0000u);
+    return make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
+                      __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
 }
 
 template <int D>
-__global__ void __launch_bounds__(kRowThreads) cache_read_kernel(const CacheRowsArgs A) {
-    constexpr int kT = D / 8;
-    const int H = A.pool.heads;
-    const long long item = (static_cast<long long>(blockIdx.x) * kRowThreads + threadIdx.x) / kT;
-    const int c = threadIdx.x % kT;
-    const long long tok = item / (2 * H);
-    const int hk = static_cast<int>(item % (2 * H));
-    const bool isv = hk >= H;
-    const int h = isv ? hk - H : hk;
-    const int b = static_cast<int>(tok / A.n), i = static_cast<int>(tok % A.n);
-    if (b >= A.B) return;
-    uint4 out = make_uint4(0, 0, 0, 0);
-    if (i < (A.count ? A.count[b] : A.n)) {
-        const long long pos = static_cast<long long>(A.start[b]) + i;
-        const int page = cache_page(A.tab, A.pool.num_pages, A.pool.p_shift, b, pos);
-        if (page >= 0) {
-            const int P = A.pool.P, slot = static_cast<int>(pos & (P - 1));
-            const unsigned char* blk = A.pool.base + page * A.pool.page_stride + h * A.pool.head_stride +
-                                       (isv ? CacheBlock<D>::v_codes(P) : 0);
-            const uint32_t w = reinterpret_cast<const uint32_t*>(blk + slot * CacheBlock<D>::kRow)[c];
-            const uint32_t sb = reinterpret_cast<const uint16_t*>(blk + P * CacheBlock<D>::kRow +
-                                                                  slot * CacheBlock<D>::kScl)[c >> 2];
-            const float s = __uint_as_float(sb << 16);
-            out = make_uint4(values2(w, s), values2(w >> 8, s), values2(w >> 16, s), values2(w >> 24, s));
-        } else if (A.status) {
-            atomicOr(A.status + b, SPEC_ST_BAD_PAGE);
+__global__ void __launch_bounds__(kRowThreads) cache_read_kernel(const CacheRowsArgs A, int heads_per) {
+    using Blk = CacheBlock<D>;
+    const RowPlace<D> at;
+    const int c = at.c, P = A.pool.P, H = A.pool.heads;
+    const int h0 = blockIdx.z * heads_per, h1 = min(h0 + heads_per, H);
+    if (at.i >= A.n) return;
+    for (int b = blockIdx.y; b < A.B; b += gridDim.y) {
+        const bool live = at.i < (A.count ? A.count[b] : A.n);
+        int page = -1;
+        long long pos = 0;
+        if (live) {
+            pos = static_cast<long long>(A.start[b]) + at.i;
+            page = cache_page(A.tab, A.pool.num_pages, A.pool.p_shift, b, pos);
+            if (page < 0 && A.status) atomicOr(A.status + b, SPEC_ST_BAD_PAGE);
+        }
+        const int slot = static_cast<int>(pos & (P - 1));
+        const unsigned char* blk = A.pool.base + page * A.pool.page_stride + (at.isv ? Blk::v_codes(P) : 0);
+        uint16_t* dst = (at.isv ? A.v_out : A.k_out) + (static_cast<long long>(b) * A.n + at.i) * H * D + c * 8;
+        for (int h = h0; h < h1; h += kFly) {
+            uint32_t w[kFly], s[kFly];
+#pragma unroll
+            for (int q = 0; q < kFly; ++q) {
+                w[q] = 0x88888888u;
+                s[q] = 0;
+                if (page >= 0 && h + q < h1) {
+                    const unsigned char* from = blk + (h + q) * A.pool.head_stride;
+                    w[q] = reinterpret_cast<const uint32_t*>(from + slot * Blk::kRow)[c];
+                    s[q] = reinterpret_cast<const uint16_t*>(from + P * Blk::kRow + slot * Blk::kScl)[c >> 2];
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < kFly; ++q) {
+                if (h + q >= h1) break;
+                const uint32_t s2 = s[q] * 0x10001u;
+                uint32_t c2;
+                asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(c2) : "r"(s2), "r"(0xBFC0BFC0u));
+                __stcs(reinterpret_cast<uint4*>(dst + static_cast<long long>(h + q) * D), values8(w[q], s2, c2));
+            }
         }
     }
-    uint16_t* dst = (isv ? A.v_out : A.k_out) + ((tok * H) + h) * D + c * 8;
-    __stcs(reinterpret_cast<uint4*>(dst), out);
 }
 
-cudaError_t row_grid(const CacheRowsArgs& A, int D, dim3& grid) {
-    const long long threads = static_cast<long long>(A.B) * A.n * A.pool.heads * 2 * (D / 8);
-    const long long blocks = (threads + kRowThreads - 1) / kRowThreads;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    grid = dim3(static_cast<unsigned>(blocks));
-    return cudaSuccess;
+// Heads are split over blockIdx.z where there are few rows: a step's rows then
+// cost one round of loads instead of H / 4.
+template <int D>
+dim3 row_grid(const CacheRowsArgs& A, int& heads_per) {
+    const int x = (A.n + RowPlace<D>::kTokens - 1) / RowPlace<D>::kTokens, y = A.B < 65535 ? A.B : 65535;
+    const long long blocks = static_cast<long long>(x) * y;
+    heads_per = A.pool.heads;
+    if (blocks < 608 && heads_per > kFly) heads_per = kFly;
+    const int z = (A.pool.heads + heads_per - 1) / heads_per;
+    return dim3(static_cast<unsigned>(x), static_cast<unsigned>(y), static_cast<unsigned>(z));
 }
 
 }  // namespace
 
 cudaError_t cache_append_run(const CacheRowsArgs& A, cudaStream_t st) {
-    dim3 grid;
-    const cudaError_t e = row_grid(A, A.pool.D, grid);
-    if (e != cudaSuccess) return e;
+    int per;
     if (A.pool.D == 128) {
-        if (A.aligned) cache_append_kernel<128, true><<<grid, kRowThreads, 0, st>>>(A);
-        else cache_append_kernel<128, false><<<grid, kRowThreads, 0, st>>>(A);
+        const dim3 grid = row_grid<128>(A, per);
+        if (A.aligned) cache_append_kernel<128, true><<<grid, kRowThreads, 0, st>>>(A, per);
+        else cache_append_kernel<128, false><<<grid, kRowThreads, 0, st>>>(A, per);
     } else {
-        if (A.aligned) cache_append_kernel<64, true><<<grid, kRowThreads, 0, st>>>(A);
-        else cache_append_kernel<64, false><<<grid, kRowThreads, 0, st>>>(A);
+        const dim3 grid = row_grid<64>(A, per);
+        if (A.aligned) cache_append_kernel<64, true><<<grid, kRowThreads, 0, st>>>(A, per);
+        else cache_append_kernel<64, false><<<grid, kRowThreads, 0, st>>>(A, per);
     }
     return cudaGetLastError();
 }
 
 cudaError_t cache_read_run(const CacheRowsArgs& A, cudaStream_t st) {
-    dim3 grid;
-    const cudaError_t e = row_grid(A, A.pool.D, grid);
-    if (e != cudaSuccess) return e;
-    if (A.pool.D == 128) cache_read_kernel<128><<<grid, kRowThreads, 0, st>>>(A);
-    else cache_read_kernel<64><<<grid, kRowThreads, 0, st>>>(A);
+    int per;
+    if (A.pool.D == 128) {
+        const dim3 grid = row_grid<128>(A, per);
+        cache_read_kernel<128><<<grid, kRowThreads, 0, st>>>(A, per);
+    } else {
+        const dim3 grid = row_grid<64>(A, per);
+        cache_read_kernel<64><<<grid, kRowThreads, 0, st>>>(A, per);
+    }
     return cudaGetLastError();
 }
 
