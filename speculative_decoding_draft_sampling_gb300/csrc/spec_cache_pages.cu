@@ -7,6 +7,8 @@
 // page numbers, never by the order in which threads arrive.  What costs
 // bandwidth, the copy of a forked request's last partial page in every layer
 // and head, is a second kernel over the whole device.
+#include <type_traits>
+
 #include "../../include/spec_cache.h"
 #include "spec_cache.cuh"
 
@@ -59,7 +61,8 @@ __device__ __forceinline__ int stack_size(const CachePagesArgs& A) {
 
 __global__ void __launch_bounds__(kPageThreads) cache_reserve_kernel(const CachePagesArgs A) {
     __shared__ int sums[kPageWarps];
-    const int lane = threadIdx.x & 31;
+    __shared__ int4 grant[kPageThreads];        // a request's pages: first of the taken, where in its row, how many
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int have = stack_size(A);
     long long asked = 0;                        // pages of all requests before this chunk
     int taken = 0;
@@ -80,23 +83,19 @@ __global__ void __launch_bounds__(kPageThreads) cache_reserve_kernel(const Cache
         if (need > 0 && !ok) bits = SPEC_ST_NO_PAGE;
         if (bits && A.status) atomicOr(A.status + r, bits);
         if (ok) A.held[r] = held + need;
-        // a warp writes the pages of its 32 requests, one request at a time
-        const int first = static_cast<int>(asked) + off;
-#pragma unroll 1
-        for (unsigned todo = __ballot_sync(0xffffffffu, ok); todo; todo &= todo - 1) {
-            const int l = __ffs(todo) - 1;
-            const int rr = r0 + static_cast<int>(threadIdx.x) - lane + l;
-            const int cnt = __shfl_sync(0xffffffffu, need, l);
-            const int at = __shfl_sync(0xffffffffu, first, l);
-            const int h = __shfl_sync(0xffffffffu, held, l);
-            for (int j = lane; j < cnt; j += 32) {
-                const int page = take_page(A, have, at + j);
+        grant[threadIdx.x] = make_int4(static_cast<int>(asked) + off, held, ok ? need : 0, 0);
+        int got;
+        block_scan(ok ? need : 0, sums, got);   // (and a barrier)
+        // the warps write the requests' pages in turn
+        for (int l = w; l < min(kPageThreads, A.R - r0); l += kPageWarps) {
+            const int4 g = grant[l];
+            for (int j = lane; j < g.z; j += 32) {
+                const int page = take_page(A, have, g.x + j);
                 if (page >= 0) A.ref[page] = 1;
-                A.table[rr * A.stride + h + j] = page;
+                A.table[(r0 + l) * A.stride + g.y + j] = page;
             }
         }
-        int got;
-        block_scan(ok ? need : 0, sums, got);
+        __syncthreads();
         taken += got;
         asked += total;
         if (asked > have) asked = static_cast<long long>(have) + 1;   // nobody behind gets a page
@@ -109,35 +108,64 @@ __global__ void __launch_bounds__(kPageThreads) cache_reserve_kernel(const Cache
 __global__ void __launch_bounds__(kPageThreads) cache_release_kernel(const CachePagesArgs A) {
     extern __shared__ uint32_t freed[];         // one bit a page
     __shared__ int sums[kPageWarps];
+    __shared__ int2 spans[kPageThreads];
+    constexpr int kFly = 4;                     // requests that a warp looks at together
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int words = (A.num_pages + 31) / 32;
     for (int i = threadIdx.x; i < words; i += kPageThreads) freed[i] = 0;
     __syncthreads();
-    for (int r = w; r < A.R; r += kPageWarps) {
-        const int held = clamp_held(A.held[r], A.width);
-        const int keep = min(held, pages_for(A.length[r], A.p_shift));
-        int bits = 0;
-        for (int j = keep + lane; j < held; j += 32) {
-            int* entry = A.table + r * A.stride + j;
-            const int page = *entry;
-            *entry = -1;
-            if (static_cast<unsigned>(page) >= static_cast<unsigned>(A.num_pages)) {
-                bits = SPEC_ST_BAD_PAGE;
-                continue;
+    for (int r0 = 0; r0 < A.R; r0 += kPageThreads) {
+        const int r = r0 + static_cast<int>(threadIdx.x);
+        int2 span = make_int2(0, 0);            // the pages that go: [x, y) of the request's
+        if (r < A.R) {
+            span.y = clamp_held(A.held[r], A.width);
+            span.x = min(span.y, pages_for(A.length[r], A.p_shift));
+            if (span.x < span.y) A.held[r] = span.x;
+        }
+        spans[threadIdx.x] = span;
+        __syncthreads();
+        // a warp has pages of several requests in flight: each is a read, an
+        // update of the page's count and a look at what it was
+        const int rows = min(kPageThreads, A.R - r0);
+        for (int l0 = w; l0 < rows; l0 += kFly * kPageWarps) {
+            int most = 0;
+#pragma unroll
+            for (int q = 0; q < kFly; ++q) {
+                const int l = l0 + q * kPageWarps;
+                if (l < rows) most = max(most, spans[l].y - spans[l].x);
             }
-            const int before = atomicSub(A.ref + page, 1);
-            if (before == 1) {
-                atomicOr(freed + (page >> 5), 1u << (page & 31));
-            } else if (before <= 0) {           // nobody held it: left as it was
-                atomicAdd(A.ref + page, 1);
-                bits = SPEC_ST_BAD_PAGE;
+            for (int j = lane; j < most; j += 32) {
+                int page[kFly], before[kFly];
+#pragma unroll
+                for (int q = 0; q < kFly; ++q) {
+                    const int l = l0 + q * kPageWarps;
+                    page[q] = -2;
+                    if (l < rows && spans[l].x + j < spans[l].y) page[q] = A.table[(r0 + l) * A.stride + spans[l].x + j];
+                }
+#pragma unroll
+                for (int q = 0; q < kFly; ++q) {
+                    before[q] = 2;
+                    if (static_cast<unsigned>(page[q]) < static_cast<unsigned>(A.num_pages))
+                        before[q] = atomicSub(A.ref + page[q], 1);
+                }
+#pragma unroll
+                for (int q = 0; q < kFly; ++q) {
+                    const int l = l0 + q * kPageWarps;
+                    if (page[q] == -2 && !(l < rows && spans[l].x + j < spans[l].y)) continue;
+                    A.table[(r0 + l) * A.stride + spans[l].x + j] = -1;
+                    bool bad = static_cast<unsigned>(page[q]) >= static_cast<unsigned>(A.num_pages);
+                    if (!bad && before[q] == 1) {
+                        atomicOr(freed + (page[q] >> 5), 1u << (page[q] & 31));
+                    } else if (!bad && before[q] <= 0) {    // nobody held it: left as it was
+                        atomicAdd(A.ref + page[q], 1);
+                        bad = true;
+                    }
+                    if (bad && A.status) atomicOr(A.status + r0 + l, SPEC_ST_BAD_PAGE);
+                }
             }
         }
-        if (bits && A.status) atomicOr(A.status + r, bits);
-        __syncwarp();
-        if (lane == 0 && keep < held) A.held[r] = keep;
+        __syncthreads();
     }
-    __syncthreads();
     int top = stack_size(A);
     for (int i0 = 0; i0 < words; i0 += kPageThreads) {
         const int i = i0 + static_cast<int>(threadIdx.x);
@@ -153,7 +181,8 @@ __global__ void __launch_bounds__(kPageThreads) cache_release_kernel(const Cache
 
 __global__ void __launch_bounds__(kPageThreads) cache_fork_kernel(const CachePagesArgs A) {
     __shared__ int sums[kPageWarps];
-    const int lane = threadIdx.x & 31;
+    __shared__ int4 shares[kPageThreads];       // parent, child, full pages shared
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int have = stack_size(A);
     int asked = 0, taken = 0;
     for (int f0 = 0; f0 < A.F; f0 += kPageThreads) {
@@ -186,31 +215,37 @@ __global__ void __launch_bounds__(kPageThreads) cache_fork_kernel(const CachePag
             if (ok) A.held[dst] = full + own;
             if (bits && A.status) atomicOr(A.status + f, bits);
         }
-        // the shared pages, one child at a time a warp
-#pragma unroll 1
-        for (unsigned todo = __ballot_sync(0xffffffffu, ok && full > 0); todo; todo &= todo - 1) {
-            const int l = __ffs(todo) - 1;
-            const int s = __shfl_sync(0xffffffffu, src, l), d = __shfl_sync(0xffffffffu, dst, l);
-            const int cnt = __shfl_sync(0xffffffffu, full, l);
-            for (int j = lane; j < cnt; j += 32) {
-                const int page = A.table[s * A.stride + j];
-                A.table[d * A.stride + j] = page;
+        shares[threadIdx.x] = make_int4(src, dst, ok ? full : 0, 0);
+        int got;
+        block_scan(ok ? own : 0, sums, got);    // (and a barrier)
+        // the shared pages: the warps take the children in turn
+#pragma unroll 4
+        for (int l = w; l < min(kPageThreads, A.F - f0); l += kPageWarps) {
+            const int4 g = shares[l];
+            for (int j = lane; j < g.z; j += 32) {
+                const int page = A.table[g.x * A.stride + j];
+                A.table[g.y * A.stride + j] = page;
                 if (static_cast<unsigned>(page) < static_cast<unsigned>(A.num_pages)) atomicAdd(A.ref + page, 1);
             }
         }
-        int got;
-        block_scan(ok ? own : 0, sums, got);
+        __syncthreads();
         taken += got;
         asked += total;
     }
     if (threadIdx.x == 0) A.num_free[0] = have - taken;
 }
 
-// One CTA copies the rows of one (fork, layer, range of heads): four runs a
-// block, codes in 16-byte vectors and scales in 4-byte words.
+// A CTA copies one fork's rows in a few (layer, head) blocks: four runs a block,
+// codes in 16-byte pieces and scales a row at a time, a piece of each of kBlocks
+// blocks in flight a thread.  It may be launched while the fork's decisions are
+// still being made.
+constexpr int kBlocks = 4;
+
 template <int D>
 __global__ void __launch_bounds__(kCopyThreads) cache_copy_kernel(const CachePagesArgs A) {
     using Blk = CacheBlock<D>;
+    using Scl = typename std::conditional<D == 128, uint2, uint32_t>::type;    // a row's scales
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int f = blockIdx.y, P = A.pool.P;
     const int to = A.new_page[f];
     if (to < 0) return;
@@ -219,23 +254,37 @@ __global__ void __launch_bounds__(kCopyThreads) cache_copy_kernel(const CachePag
     const int rows = len & (P - 1);
     const int from = A.table[src * A.stride + (len >> A.p_shift)];
     if (static_cast<unsigned>(from) >= static_cast<unsigned>(A.num_pages)) return;
-    const int codes = rows * Blk::kRow / 16, scales = rows * Blk::kScl / 4;
-    const int per = 2 * (codes + scales);
+    const int codes = rows * Blk::kRow / 16, half = codes + rows;
     const int pairs = A.pool.layers * A.pool.heads;
-    for (int pair = blockIdx.x; pair < pairs; pair += gridDim.x) {
-        const int layer = pair / A.pool.heads, head = pair % A.pool.heads;
-        unsigned char* base = A.pool.base + layer * A.pool.layer_stride + head * A.pool.head_stride;
-        const unsigned char* a = base + from * A.pool.page_stride;
-        unsigned char* z = base + to * A.pool.page_stride;
-        for (int w = threadIdx.x; w < per; w += kCopyThreads) {
-            const int half = w >= codes + scales ? w - (codes + scales) : w;
-            int at = half == w ? 0 : Blk::v_codes(P);
-            if (half < codes) {
-                at += half * 16;
-                *reinterpret_cast<uint4*>(z + at) = *reinterpret_cast<const uint4*>(a + at);
+    const long long move = (static_cast<long long>(to) - from) * A.pool.page_stride;
+    for (int p0 = blockIdx.x * kBlocks; p0 < pairs; p0 += gridDim.x * kBlocks) {
+        unsigned char* blk[kBlocks];
+#pragma unroll
+        for (int q = 0; q < kBlocks; ++q) {
+            const int layer = (p0 + q) / A.pool.heads, head = (p0 + q) % A.pool.heads;
+            blk[q] = A.pool.base + layer * A.pool.layer_stride + head * A.pool.head_stride + from * A.pool.page_stride;
+        }
+        for (int w = threadIdx.x; w < 2 * half; w += kCopyThreads) {
+            const int x = w >= half ? w - half : w;
+            int at = w >= half ? Blk::v_codes(P) : 0;
+            if (x < codes) {
+                at += x * 16;
+                uint4 r[kBlocks];
+#pragma unroll
+                for (int q = 0; q < kBlocks; ++q)
+                    if (p0 + q < pairs) r[q] = __ldcs(reinterpret_cast<const uint4*>(blk[q] + at));
+#pragma unroll
+                for (int q = 0; q < kBlocks; ++q)
+                    if (p0 + q < pairs) *reinterpret_cast<uint4*>(blk[q] + at + move) = r[q];
             } else {
-                at += P * Blk::kRow + (half - codes) * 4;
-                *reinterpret_cast<uint32_t*>(z + at) = *reinterpret_cast<const uint32_t*>(a + at);
+                at += P * Blk::kRow + (x - codes) * Blk::kScl;
+                Scl r[kBlocks];
+#pragma unroll
+                for (int q = 0; q < kBlocks; ++q)
+                    if (p0 + q < pairs) r[q] = *reinterpret_cast<const Scl*>(blk[q] + at);
+#pragma unroll
+                for (int q = 0; q < kBlocks; ++q)
+                    if (p0 + q < pairs) *reinterpret_cast<Scl*>(blk[q] + at + move) = r[q];
             }
         }
     }
@@ -250,7 +299,7 @@ cudaError_t cache_reserve_run(const CachePagesArgs& A, cudaStream_t st) {
 
 cudaError_t cache_release_run(const CachePagesArgs& A, cudaStream_t st) {
     const size_t smem = static_cast<size_t>((A.num_pages + 31) / 32) * 4;
-    if (smem > 48 * 1024) {
+    if (smem > 32 * 1024) {                     // (beside the static arrays)
         const cudaError_t e = cudaFuncSetAttribute(cache_release_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    kCacheMaxPages / 8);
         if (e != cudaSuccess) return e;
@@ -263,10 +312,19 @@ cudaError_t cache_fork_run(const CachePagesArgs& A, cudaStream_t st) {
     cache_fork_kernel<<<1, kPageThreads, 0, st>>>(A);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const dim3 grid(static_cast<unsigned>(A.pool.layers * A.pool.heads), static_cast<unsigned>(A.F));
-    if (A.pool.D == 128) cache_copy_kernel<128><<<grid, kCopyThreads, 0, st>>>(A);
-    else cache_copy_kernel<64><<<grid, kCopyThreads, 0, st>>>(A);
-    return cudaGetLastError();
+    // the copy waits for the decisions on the device, not for their launch's end
+    const int pairs = A.pool.layers * A.pool.heads;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((pairs + kBlocks - 1) / kBlocks), static_cast<unsigned>(A.F));
+    cfg.blockDim = dim3(kCopyThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return A.pool.D == 128 ? cudaLaunchKernelEx(&cfg, cache_copy_kernel<128>, A)
+                           : cudaLaunchKernelEx(&cfg, cache_copy_kernel<64>, A);
 }
 
 }  // namespace spec
