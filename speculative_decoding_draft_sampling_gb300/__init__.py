@@ -596,6 +596,14 @@ def adaptive_len(conf, a: float, b: float, *, cost=None, out: Optional[AdaptiveL
 # ---------------------------------------------------------------------------
 # the paged 4-bit cache
 # ---------------------------------------------------------------------------
-from .cache import (ST_BAD_PAGE, ST_NO_PAGE, CacheAttention, PageState, cache_append, cache_attend,  # noqa: E402
-                    cache_block_bytes, cache_compact, cache_fork, cache_read, cache_release, cache_reserve,
-                    page_state)
+from . import cache  # noqa: E402
+from .cache import ST_BAD_PAGE, ST_NO_PAGE, CacheAttention, PageState, cache_block_bytes, page_state  # noqa: E402
+
+
+def __getattr__(name: str):
+    """The cache calls are the binding's own functions, put in place at the
+    first use of one (importing the package loads no library)."""
+    if name in cache.CALLS:
+        cache.bind((globals(), cache.__dict__))
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,6 +1,7 @@
 """Builds libspecverify.so in-tree: every .cu under csrc/ compiled for
 sm_103a (one -gencode, -lineinfo) in parallel, then linked with the static
-CUDA runtime."""
+CUDA runtime; and beside it _spec_torch.so, the cache calls' Python binding
+(g++, against the installed PyTorch)."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -8,11 +9,14 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIBDIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIBDIR, "libspecverify.so")
+BINDING = os.path.join(LIBDIR, "_spec_torch.so")
+BINDING_SRC = os.path.join(CSRC, "spec_torch.cpp")
 ROOT = os.path.dirname(HERE)
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -42,10 +46,45 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def binding_up_to_date() -> bool:
+    if not os.path.exists(BINDING):
+        return False
+    t = os.path.getmtime(BINDING)
+    return all(os.path.getmtime(p) <= t for p in [BINDING_SRC] + glob.glob(os.path.join(ROOT, "include", "*.h")))
+
+
+def build_binding() -> str:
+    """Compile the cache calls' Python binding (no device code)."""
+    import torch
+    top = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I", os.path.join(top, "include"),
+           "-I", os.path.join(top, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"), BINDING_SRC, "-o", tmp,
+           "-L", os.path.join(top, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
+    os.makedirs(LIBDIR, exist_ok=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=(), out: str = None) -> str:
     """Build the library (to `out` with `extra_flags` for a development
     variant, e.g. -DSPEC_TRACE; the default is the product library)."""
     lib = out or LIB
+    with cf.ThreadPoolExecutor(max_workers=1) as one:
+        stale = out is None and (force or not binding_up_to_date())
+        binding = one.submit(build_binding) if stale else None     # beside the kernels' compilation
+        lib = _build_library(force, verbose, extra_flags, lib, out)
+        if binding is not None:
+            binding.result()
+    return lib
+
+
+def _build_library(force, verbose, extra_flags, lib, out) -> str:
     if not force and out is None and up_to_date():
         return LIB
     objdir = os.path.join(os.path.dirname(lib), "obj" if out is None else "obj_" + os.path.basename(lib))
