@@ -12,12 +12,6 @@
 // passes it by more than 2^8; until then weights may reach 2^8, which changes
 // nothing in fp32 and costs one comparison a score.
 //
-// Work.  A unit is (request, kv head, block of 8 * NT rows); its keys are cut
-// into tiles of 64 tokens.  All tiles of all units, in order, are dealt out in
-// equal contiguous shares to a grid that fills the device once, whatever the
-// requests' lengths; a unit that several CTAs share is joined by the last of
-// them to finish, in CTA order (so the bits do not depend on timing).
-//
 // A tile.  Bulk copies (TMA), one per page block, bring a tile into a ring in
 // shared memory.  Codes go from there straight into the registers of the tensor
 // instruction (mma m16n8k16): scores are computed transposed, S^T = K Q^T and
@@ -27,15 +21,10 @@
 // gone through shared memory, a quarter of the D rows of O^T over all 64
 // tokens.  No code is decoded twice, a warp's share of O^T is small enough for
 // many CTAs an SM, and one barrier a tile is all they wait for each other.
-#include <cuda_bf16.h>
-#include <math_constants.h>
-
 #include <atomic>
 #include <type_traits>
 
-#include "../../include/spec_cache.h"
-#include "spec_cache.cuh"
-#include "spec_common.cuh"
+#include "spec_cache_attend.cuh"
 
 namespace spec {
 
@@ -44,99 +33,8 @@ namespace {
 constexpr int kAtWarps = 4;
 constexpr int kAtThreads = 32 * kAtWarps;
 constexpr int kTile = 64;                       // tokens a tile
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kNoMax = -3.0e38f;              // the maximum before any key
-constexpr float kSlack = 8.0f;                  // how far (in powers of two) a score may pass the maximum
+constexpr int kFewRows = 16;                    // rows a kv head that this kernel takes
 
-// ---------------------------------------------------------------------------
-// the workspace and the shares of the work
-// ---------------------------------------------------------------------------
-// control words (zero before the first call; every call leaves `arrived` zero)
-struct AttendCtrl {
-    uint32_t pad0;
-    uint32_t error;                             // SPEC_WS_ERR_WAIT, where spec_workspace_error reads it
-    uint32_t pad1[62];
-    uint32_t arrived[(SPEC_CACHE_WS_CONTROL - 256) / 4];   // per CTA: parts done of the unit that starts in it
-};
-
-static_assert(sizeof(AttendCtrl) == SPEC_CACHE_WS_CONTROL, "the control words");
-constexpr int kMaxGrid = (SPEC_CACHE_WS_CONTROL - 256) / 4;
-
-struct AttendPlan {
-    uint32_t one2;                              // 0x3F803F80 (codes2)
-    int grid;                                   // CTAs
-    int row_tiles;                              // blocks of 8 * NT rows a (request, kv head)
-    int min_tiles;                              // tiles worth a CTA
-    float* ml;                                  // [2 * grid][8 * NT][4]: m, l, l of the rounded weights
-    float* part;                                // [2 * grid][8 * NT][D]
-    AttendCtrl* ctrl;
-};
-
-// What a request asks for.
-struct Req {
-    int ctx, rows, len;                         // len = ctx + rows
-    int first;                                  // tiles [0, sink_tiles) and [first, tiles) hold visible keys
-    int sink_tiles, tiles;                      // tiles: of the whole context
-    int low;                                    // positions below are outside every row's window (sinks aside)
-    __device__ __forceinline__ int visited() const { return max(1, sink_tiles + tiles - first); }
-    __device__ __forceinline__ int real(int v) const { return v < sink_tiles ? v : first + (v - sink_tiles); }
-};
-
-// its context and rows as given
-__device__ __forceinline__ int2 request_len(const CacheAttendArgs& A, int b) {
-    return make_int2(A.ctx[b], A.rows ? A.rows[b] : A.n);
-}
-__device__ __forceinline__ Req request(const CacheAttendArgs& A, int2 given) {
-    Req r;
-    const long long room = static_cast<long long>(A.tab.width) << A.pool.p_shift;
-    r.ctx = static_cast<int>(min(static_cast<long long>(max(given.x, 0)), room));
-    r.rows = min(max(given.y, 0), A.n);
-    r.len = r.rows ? r.ctx + r.rows : 0;
-    r.tiles = (r.len + kTile - 1) / kTile;
-    r.low = 0;
-    r.sink_tiles = 0;
-    r.first = 0;
-    if (A.window > 0) {
-        r.low = max(0, r.ctx - A.window + 1);
-        r.sink_tiles = min(r.tiles, (min(A.sinks, r.len) + kTile - 1) / kTile);
-        r.first = min(max(r.low / kTile, r.sink_tiles), r.tiles);
-    }
-    return r;
-}
-
-// tiles of one kv head of a request: blocks of rows that hold no row cost one
-__device__ __forceinline__ int head_work(const CacheAttendArgs& A, const Req& r, int row_tiles, int rows_a_tile) {
-    const int live = (r.rows * A.G + rows_a_tile - 1) / rows_a_tile;
-    return live * r.visited() + (row_tiles - live);
-}
-
-// ---------------------------------------------------------------------------
-// codes to bf16
-// ---------------------------------------------------------------------------
-// Two codes that lie 16 bits apart (at 4i and 4i + 16) as bf16: placed at bits
-// 3..6 of the significand under the exponent of 1 they are 1 + code/16, and one
-// fused multiply-add with (s, -1.5 s) gives (code - 8)/16 * s, exactly (a scale
-// has five significant bits, so 1.5 s fits too).  The factor 16 goes into the
-// softmax scale (K) and the final division (V).  one2 is 0x3F803F80, the two
-// ones' bits, out of the kernel's parameters: as a literal beside the mask's it
-// costs a second logic instruction, the pipe that these kernels fill first
-// (4 x 131072 tokens: 144 against 128 us).
-template <int I>
-__device__ __forceinline__ uint32_t codes2(uint32_t w, uint32_t s2, uint32_t c2, uint32_t one2) {
-    uint32_t t;
-    if constexpr (I == 0) t = w << 3;
-    else t = w >> (4 * I - 3);
-    t = (t & 0x00780078u) | one2;
-    uint32_t v;
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(v) : "r"(t), "r"(s2), "r"(c2));
-    return v;
-}
-__device__ __forceinline__ uint32_t minus1_5(uint32_t s2) {
-    uint32_t v;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(v) : "r"(s2), "r"(0xBFC0BFC0u));
-    return v;
-}
 __device__ __forceinline__ uint32_t lds16(uint32_t a) {
     unsigned short v;
     asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
@@ -178,62 +76,10 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float exp2_fast(float x) {
-    float v;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(v) : "f"(x));
-    return v;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    uint32_t v;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(hi), "f"(lo));
-    return v;
-}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t v;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(v) : "r"(x));
     return v;
-}
-
-// bits [a, b) of a tile that starts at t0
-__device__ __forceinline__ unsigned long long range64(long long a, long long b, long long t0) {
-    const int lo = static_cast<int>(min(max(a - t0, 0ll), 64ll)), hi = static_cast<int>(min(max(b - t0, 0ll), 64ll));
-    if (hi <= lo) return 0;
-    return (hi == 64 ? ~0ull : (1ull << hi) - 1ull) & ~((1ull << lo) - 1ull);
-}
-
-// The keys of the tile at t0 that row i of request b sees.
-__device__ __forceinline__ unsigned long long seen64(const CacheAttendArgs& A, const Req& r, int b, int i, int t0) {
-    const long long at = static_cast<long long>(b) * A.n;
-    const int p = r.ctx + (A.depth ? min(max(A.depth[at + i], 0), A.n) : i);
-    unsigned long long drafted = 0, context;
-    if (!A.mask) {
-        context = range64(0, r.ctx + min(i + 1, r.rows), t0);
-    } else {
-        context = range64(0, r.ctx, t0);
-        const int off = t0 - r.ctx;             // drafted row at the tile's first token
-        if (off + kTile > 0) {
-            const int W = (A.n + 63) >> 6;
-            const unsigned long long* m = A.mask + (at + i) * W;
-            if (off < 0) {
-                drafted = m[0] << -off;
-            } else {
-                const int w = off >> 6, s = off & 63;
-                if (w < W) drafted = m[w] >> s;
-                if (s && w + 1 < W) drafted |= m[w + 1] << (64 - s);
-            }
-            drafted &= range64(r.ctx, r.len, t0);
-            if (A.window > 0)
-                for (unsigned long long x = drafted; x; x &= x - 1) {
-                    const int bit = __ffsll(static_cast<long long>(x)) - 1;
-                    const int j = off + bit;
-                    const int key = r.ctx + (A.depth ? min(max(A.depth[at + j], 0), A.n) : j);
-                    if (p - key >= A.window && key >= A.sinks) drafted &= ~(1ull << bit);
-                }
-        }
-    }
-    if (A.window > 0)
-        context &= range64(static_cast<long long>(p) - A.window + 1, 1ll << 40, t0) | range64(0, A.sinks, t0);
-    return context | drafted;
 }
 
 // ---------------------------------------------------------------------------
@@ -264,9 +110,7 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
     constexpr int kMT = D / 64;                 // 16-row blocks of O^T that a warp holds
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ uint64_t full[kS];
-    __shared__ long long s_sum[kAtWarps];
-    __shared__ long long s_found[2];
-    __shared__ int2 s_len[kAtThreads];          // the first requests' lengths
+    __shared__ ShareScratch<kAtWarps> s_share;
     __shared__ long long s_out[kRows];          // a row's place in out and lse (-1: none)
     __shared__ uint32_t s_there[kS];            // which page blocks of a stage's tile are there
     __shared__ unsigned long long s_seen[kRows];
@@ -277,7 +121,6 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);    // uniform to the compiler too
     const int r8 = lane >> 2, c4 = lane & 3;
-    const int H = A.pool.heads;
     const int P = A.pool.P, p_shift = A.pool.p_shift;
     const int ppt_shift = 6 - p_shift, ppt = 1 << ppt_shift;    // page blocks a tile
     // A tile in shared memory is laid out like one block of 64 tokens, whatever
@@ -293,76 +136,9 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
         s_dead = 0;
     }
 
-    // ---- this CTA's share: [lo, hi) of all tiles ---------------------------
-    int2 given = make_int2(0, 0);
-    auto work_of = [&](int b) {
-        if (b >= A.B) return 0ll;
-        given = request_len(A, b);
-        return static_cast<long long>(H) * head_work(A, request(A, given), L.row_tiles, kRows);
-    };
-    // the requests a chunk of threads at a time; one chunk is the usual case
-    long long total = 0, first_work = 0;
-    for (int b0 = 0; b0 < A.B; b0 += kAtThreads) {
-        const long long v = work_of(b0 + tid);
-        if (b0 == 0) {
-            first_work = v;
-            s_len[tid] = given;
-        }
-        total += v;
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    if (lane == 0) s_sum[warp] = total;
-    __syncthreads();
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < kAtWarps; ++w) total += s_sum[w];
-    const long long units = static_cast<long long>(A.B) * H * L.row_tiles;
-    long long want = total / L.min_tiles;
-    if (want > units * 64) want = units * 64;   // what joins a unit must stay small beside it
-    const int active = static_cast<int>(min(static_cast<long long>(gridDim.x), max(want, 1ll)));
+    Share<kTile, kAtWarps> share(A, L, s_share, kRows);
+    if (share.lo == share.hi) return;
     const int cta = blockIdx.x;
-    if (cta >= active) return;
-    // quotients of 64 bits only where the work needs them
-    auto start_of = [&](long long c) {
-        const long long x = c * total;
-        return x >> 32 ? x / active : static_cast<long long>(static_cast<unsigned>(x) / static_cast<unsigned>(active));
-    };
-    const long long lo = start_of(cta), hi = start_of(cta + 1);
-    __syncthreads();
-    // the request that holds tile lo, and where its tiles start
-    {
-        long long before = 0;
-        for (int b0 = 0; b0 < A.B; b0 += kAtThreads) {
-            const long long v = b0 == 0 ? first_work : work_of(b0 + tid);
-            long long inc = v;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long t = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += t;
-            }
-            if (lane == 31) s_sum[warp] = inc;
-            __syncthreads();
-            long long base = before, all = 0;
-#pragma unroll
-            for (int w = 0; w < kAtWarps; ++w) {
-                if (w < warp) base += s_sum[w];
-                all += s_sum[w];
-            }
-            const long long from = base + inc - v;
-            if (v > 0 && from <= lo && lo < from + v) {
-                s_found[0] = b0 + tid;
-                s_found[1] = from;
-            }
-            __syncthreads();
-            before += all;
-            if (lo < before) break;
-        }
-    }
-    int b = static_cast<int>(s_found[0]);
-    long long b_from = s_found[1];
-    auto req_at = [&](int i) { return request(A, i < kAtThreads ? s_len[i] : request_len(A, i)); };
-    Req rq = req_at(b);
 
     uint32_t phases = 0;                        // one bit a stage
     const int tok = r8 ^ ((r8 >> 1) & 1);       // the token (of 8) that is row r8 of S^T
@@ -381,55 +157,16 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
     const float cs = A.scale * kLog2e * 16.0f;
     const uint32_t one2 = L.one2;
 
-    // ---- a unit, or the part of it that falls into this CTA's share ----------
-    struct Seg {
-        int b, h, row0, live_rows;              // request, kv head, first row, rows that are there
-        int v0, v1, tiles_u;                    // tiles [v0, v1) of the unit's
-        int tiles;                              // v1 - v0, or 0 where no row is there
-        long long u_from;                       // the unit's first tile among all
-    };
-    // the unit that holds tile pos (moves rq on to its request)
-    auto segment = [&](long long pos) {
-        Seg g;
-        int per_head = head_work(A, rq, L.row_tiles, kRows);
-        while (pos - b_from >= static_cast<long long>(per_head) * H) {
-            b_from += static_cast<long long>(per_head) * H;
-            rq = req_at(++b);
-            per_head = head_work(A, rq, L.row_tiles, kRows);
-        }
-        const unsigned in_req = static_cast<unsigned>(pos - b_from);
-        g.b = b;
-        g.h = in_req / static_cast<unsigned>(per_head);
-        const int in_head = in_req - static_cast<unsigned>(g.h) * per_head;
-        const int live = (rq.rows * A.G + kRows - 1) / kRows;
-        const int visited = rq.visited();
-        int rt;
-        if (in_head < live * visited) {
-            rt = static_cast<unsigned>(in_head) / static_cast<unsigned>(visited);
-            g.tiles_u = visited;
-            g.v0 = in_head - rt * visited;
-        } else {
-            rt = live + in_head - live * visited;
-            g.tiles_u = 1;
-            g.v0 = 0;
-        }
-        g.u_from = pos - g.v0;
-        g.v1 = static_cast<int>(min(static_cast<long long>(g.tiles_u), hi - g.u_from));
-        g.row0 = rt * kRows;
-        g.live_rows = min(max(rq.rows * A.G - g.row0, 0), kRows);
-        g.tiles = g.live_rows > 0 ? g.v1 - g.v0 : 0;
-        return g;
-    };
     // Copies, by warp 0: a lane per page block of the coming tiles.
     int entry = -2;
-    auto issue = [&](const Seg& g, int k, int s) {
+    auto issue = [&](const Segment& g, int k, int s) {
         const int in = k & ((32 >> ppt_shift) - 1);         // of the tiles whose page ids the lanes hold
         if (in == 0) {
             const int v = g.v0 + k + (lane >> ppt_shift);
             entry = -2;
             if (v < g.v1) {
-                const int t = rq.real(v) * kTile + ((lane & (ppt - 1)) << p_shift);
-                if (t < rq.len && (A.window == 0 || t < A.sinks || t + P > rq.low)) {
+                const int t = share.rq.real(v) * kTile + ((lane & (ppt - 1)) << p_shift);
+                if (share.rq.needs(A, t, t + P)) {
                     entry = cache_page(A.tab, A.pool.num_pages, p_shift, g.b, t);
                     if (entry < 0 && A.status) atomicOr(A.status + g.b, SPEC_ST_BAD_PAGE);
                 }
@@ -458,7 +195,7 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
     };
     // The start of a segment, as far as it can run beside the end of the one
     // before it: first copies, and Q's rows into the buffer of P^T.
-    auto begin = [&](const Seg& g) {
+    auto begin = [&](const Segment& g) {
         if (warp == 0 && !s_dead)
 #pragma unroll
             for (int s = 0; s < kS; ++s)
@@ -476,12 +213,12 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
         }
     };
 
-    Seg g = segment(lo);
+    Segment g = share.segment(share.lo);
     begin(g);
     for (;;) {
         // ---- Q, laid out like the keys' words -------------------------------
         const int row0 = g.row0, live_rows = g.live_rows, tiles = g.tiles, v0 = g.v0;
-        const Req rc = rq;                      // the request (rq moves on before the segment's end)
+        const Req<kTile> rc = share.rq;         // the request (the cursor moves on before the segment's end)
         if (tid < kRows) {
             const int rho = row0 + tid, i = static_cast<unsigned>(rho) / static_cast<unsigned>(A.G);
             s_out[tid] = rho < A.n * A.G ? (static_cast<long long>(g.b) * A.n + i) * A.hq + static_cast<long long>(g.h) * A.G + rho - i * A.G : -1;
@@ -545,8 +282,7 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
             const uint32_t stage = ring + s * Cfg::kStageBytes;
             const uint32_t pbuf = p_base + (k & 1) * Cfg::kP;
             // every row sees every key of most tiles
-            const bool masked = t0 + kTile > rc.ctx || there != (1u << ppt) - 1u ||
-                                (A.window > 0 && t0 + kTile > A.sinks && t0 < rc.low + A.n);
+            const bool masked = rc.partial(A, t0) || there != (1u << ppt) - 1u;
             auto tile = [&](auto is_masked) {
                 constexpr bool kMasked = decltype(is_masked)::value;
                 unsigned long long any = ~0ull;
@@ -758,27 +494,16 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
             }
         __syncthreads();
         // every warp is past its last tile: the next segment may begin
-        const Seg cur = g;
-        const bool more = cur.u_from + cur.v1 < hi;
+        const Segment cur = g;
+        const bool more = cur.u_from + cur.v1 < share.hi;
         if (more) {
-            g = segment(cur.u_from + cur.v1);
+            g = share.segment(cur.u_from + cur.v1);
             begin(g);
         }
-        const bool whole = v0 == 0 && cur.v1 == cur.tiles_u;
+        const bool whole = cur.whole();
         // the CTA that holds the unit's first tile, and how many share it
         int c0 = cta, parts = 1;
-        if (!whole) {
-            auto cta_of = [&](long long x) {
-                const long long y = x * active;
-                int c = static_cast<int>((y | total) >> 32 ? y / total
-                                                           : static_cast<unsigned>(y) / static_cast<unsigned>(total));
-                while (start_of(c + 1) <= x) ++c;
-                while (start_of(c) > x) --c;
-                return c;
-            };
-            c0 = v0 == 0 ? cta : cta_of(cur.u_from);
-            parts = (cur.v1 == cur.tiles_u ? cta : cta_of(cur.u_from + cur.tiles_u - 1)) - c0 + 1;
-        }
+        if (!whole) share.sharers(cur, c0, parts);
         const int slot = 2 * cta + (c0 == cta ? 1 : 0);
         const int d0 = warp * (D / 4) + r8 * (D / 32);          // this lane's D/32 values of a row
         // D/32 values from d on of a row, times f, into the output
@@ -889,7 +614,9 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
     }
 }
 
-int device() {
+}  // namespace
+
+int attend_device() {
     int d = 0;
     if (cudaGetDevice(&d) != cudaSuccess) {
         cudaGetLastError();
@@ -898,9 +625,9 @@ int device() {
     return d;
 }
 
-int sm_count() {
+int attend_sms() {
     static std::atomic<int> known[64];
-    const int d = device();
+    const int d = attend_device();
     if (d >= 64) return 152;
     int v = known[d].load(std::memory_order_relaxed);
     if (v == 0) {
@@ -913,6 +640,8 @@ int sm_count() {
     return v;
 }
 
+namespace {
+
 // Blocks of 8 rows that a CTA holds at once.  The whole of R where it fits: a
 // tile's codes are decoded once for all rows.  Beyond 12 blocks, what the registers hold,
 // the rows are cut into equal parts.
@@ -924,24 +653,11 @@ int row_blocks(int R) {
     return 12;
 }
 
-size_t up256(size_t x) { return (x + 255) / 256 * 256; }
-
-struct Layout {
-    size_t ml, part, bytes;
-};
-Layout layout_of(int grid, int NT, int D) {
-    Layout y;
-    y.ml = SPEC_CACHE_WS_CONTROL;
-    y.part = y.ml + up256(static_cast<size_t>(grid) * 2 * 8 * NT * 4 * 4);
-    y.bytes = y.part + static_cast<size_t>(grid) * 2 * 8 * NT * D * 4;
-    return y;
-}
-
 template <int D, int NT>
 cudaError_t attend(const CacheAttendArgs& A, cudaStream_t st) {
     using Cfg = AttendCfg<D, NT>;
-    const int grid = min(sm_count() * Cfg::kCtas, kMaxGrid);
-    const Layout y = layout_of(grid, NT, D);
+    const int grid = min(attend_sms() * Cfg::kCtas, kMaxGrid);
+    const AttendLayout y(2 * grid, Cfg::kRows, D);
     AttendPlan L;
     L.one2 = 0x3F803F80u;
     L.grid = grid;
@@ -956,7 +672,7 @@ cudaError_t attend(const CacheAttendArgs& A, cudaStream_t st) {
     L.part = reinterpret_cast<float*>(ws + y.part);
     // the kernel's shared memory is set once a device
     static std::atomic<unsigned long long> ready{0};
-    const int dev = device();
+    const int dev = attend_device();
     if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
         const cudaError_t e = cudaFuncSetAttribute(cache_attend_kernel<D, NT>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
@@ -985,11 +701,14 @@ cudaError_t attend_rows(const CacheAttendArgs& A, cudaStream_t st) {
 
 size_t cache_attend_ws(int B, int n, int hq, int hkv, int D) {
     (void)B;
-    const int NT = row_blocks(n * (hq / hkv));
-    return layout_of(min(sm_count() * ctas_of(NT), kMaxGrid), NT, D).bytes;
+    const int R = n * (hq / hkv);
+    if (R > kFewRows) return attend_tc_ws(R, D);
+    const int NT = row_blocks(R);
+    return AttendLayout(2 * min(attend_sms() * ctas_of(NT), kMaxGrid), 8 * NT, D).bytes;
 }
 
 cudaError_t cache_attend_run(const CacheAttendArgs& A, cudaStream_t st) {
+    if (A.n * A.G > kFewRows) return attend_tc_run(A, st);
     return A.pool.D == 128 ? attend_rows<128>(A, st) : attend_rows<64>(A, st);
 }
 

@@ -1,0 +1,739 @@
+// spec_cache_attend_tc.cu -- attention over the paged 4-bit cache for requests
+// with many rows a kv head (draft trees, long chains): tcgen05.
+//
+// [SD-survey] = "大模型投机解码：Medusa、MTP、EAGLE、DFlash、DDTree 与 DSpark"
+// (Speculative decoding for LLMs: Medusa, MTP, EAGLE, DFlash, DDTree and
+// DSpark), chzhyang.github.io, §5 "DDTree".
+//
+// The mathematics is that of spec_cache_attend.cu; the shape is the other way
+// round: rows are the 128-row operand, S = Q K^T and O = P V, so that a thread
+// owns a row of S in tensor memory and the softmax needs no exchange.
+//
+// One CTA an SM, in five warp groups (the fifth for one thread) that never wait
+// for each other all at once:
+//   warps 8-11   read the codes of a tile's 128 keys, a token a thread, two
+//                tiles ahead in registers, and write them as bf16 into shared
+//                memory (128-byte swizzle); warps 12-15 the same for the values;
+//   warp 16      one thread issues the tensor work: S_g = Q K^T (both in shared
+//                memory) and O_g += P_g V with P_g in tensor memory where S_g was;
+//   warps 0-3, 4-7  two softmax groups, g = 0 and 1, each with its own S, P, O in
+//                tensor memory, so that one group's exponentials run beside the
+//                other's products.  With up to 128 rows (MT = 1) the groups take
+//                alternate tiles and their halves are joined at a unit's end; with
+//                more (MT = 2) each takes 128 of the rows and they share a tile's
+//                decoded keys and values.
+// What bounds it, a tile of 128 tokens: shared memory, 64 KB written and 96 KB
+// (MT = 1) or 192 KB read by the tensor core at 128 bytes a cycle; the tensor core
+// itself, 1024 or 2048 cycles at D = 128.
+#include <atomic>
+#include <type_traits>
+
+#include "spec_cache_attend.cuh"
+
+namespace spec {
+
+namespace {
+
+constexpr int kTok = 128;                       // tokens a tile
+constexpr int kWarps = 20;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kMmaWarp = 16;
+// Registers a thread: 96 at launch (640 threads), then moved from the decoders and
+// the issuing group to the softmax: 256 * 80 + 128 * 56 + 256 * 128 = 60416 of the
+// 61440 that the block was launched with.
+constexpr int kRegsDecode = 80, kRegsIssue = 56, kRegsSoftmax = 128;
+static_assert(256 * kRegsDecode + 128 * kRegsIssue + 256 * kRegsSoftmax <= 96 * kThreads, "register shares");
+
+template <int D, int MT>
+struct TcCfg {
+    static constexpr int kRows = 128 * MT;
+    static constexpr int kTileBytes = kTok * D * 2;         // a tile's keys or values in bf16
+    static constexpr int kQBytes = 128 * D * 2;             // 128 rows of Q
+    static constexpr int kJoin = MT == 1 ? 128 * 64 * 4 : 0;    // half a block of O, where groups are joined
+    static constexpr int kSmem = 4 * kTileBytes + MT * kQBytes + kJoin + 1024;
+};
+
+// tensor memory, in columns: S (P) of the groups, then O
+constexpr uint32_t kS(int g) { return 128 * g; }
+constexpr uint32_t kO(int g) { return 256 + 128 * g; }
+
+// ---------------------------------------------------------------------------
+// tcgen05
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void tc_alloc(uint32_t* to, uint32_t columns) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_u32(to)), "r"(columns) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tc_dealloc(uint32_t at, uint32_t columns) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(at), "r"(columns));
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(smem_u32(bar)) : "memory");
+}
+// D = A B (+ D): both operands in shared memory, or A in tensor memory
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add) : "memory");
+}
+__device__ __forceinline__ void tc_mma_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(add) : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tc_ld32(float (&x)[32], uint32_t at) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(x);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(at));
+}
+__device__ __forceinline__ void tc_st32(uint32_t at, const float (&x)[32]) {
+    const uint32_t* r = reinterpret_cast<const uint32_t*>(x);
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+        :: "r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+           "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+           "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+           "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t at, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+        :: "r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+           "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// A matrix in shared memory in 64-element (128-byte) chunks of 128 rows, 128-byte
+// swizzle: 8-row groups lie 1024 bytes apart, chunks 16384.
+__device__ __forceinline__ uint64_t tc_desc(uint32_t addr) {
+    return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(16384 >> 4) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+// kind::f16: fp32 accumulators, bf16 operands, M = 128, N columns; tb: B lies
+// with its N index contiguous
+constexpr uint32_t tc_idesc(int N, bool tb) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (tb ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
+           (static_cast<uint32_t>(128 >> 4) << 24);
+}
+constexpr int kChunk = 16384;                   // bytes of 64 columns of 128 rows
+
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+// where piece j (8 elements, 16 bytes) of row r lies in such a matrix
+__device__ __forceinline__ uint32_t piece_at(int r, int j) {
+    return (j >> 3) * kChunk + r * 128 + (((j & 7) ^ (r & 7)) << 4);
+}
+
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N)); }
+__device__ __forceinline__ void group_sync(int g) {
+    asm volatile("bar.sync %0, 128;" :: "r"(1 + g) : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// the kernel
+// ---------------------------------------------------------------------------
+struct TcBars {
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];      // a tile's keys, values
+    uint64_t s_full[2], p_full[2], o_done[2], o_free[2];        // by group
+    uint64_t q_full, q_empty;
+};
+
+template <int D, int MT>
+__global__ void __launch_bounds__(kThreads, 1)
+cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_constant__ AttendPlan L) {
+    using Cfg = TcCfg<D, MT>;
+    using Blk = CacheBlock<D>;
+    constexpr int kTile = Cfg::kTileBytes;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ TcBars bars;
+    __shared__ ShareScratch<kWarps> s_share;
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int s_dead;
+    __shared__ int s_last[2];
+    __shared__ float s_join[MT == 1 ? 128 : 1][3];
+
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const int P = A.pool.P, p_shift = A.pool.p_shift;
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t v_buf = base, k_buf = base + 2 * kTile, q_buf = base + 4 * kTile, join = q_buf + MT * Cfg::kQBytes;
+
+    Share<kTok, kWarps> share(A, L, s_share, Cfg::kRows);
+    if (share.lo == share.hi) return;
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.k_full[i], 4);
+            mbar_init(&bars.k_empty[i], 1);
+            mbar_init(&bars.v_full[i], 4);
+            mbar_init(&bars.v_empty[i], 1);
+            mbar_init(&bars.s_full[i], 1);
+            mbar_init(&bars.p_full[i], 4);
+            mbar_init(&bars.o_done[i], 1);
+            mbar_init(&bars.o_free[i], 4);
+        }
+        mbar_init(&bars.q_full, 8);
+        mbar_init(&bars.q_empty, 1);
+        fence_mbar_init();
+        s_dead = 0;
+    }
+    if (warp == kMmaWarp) tc_alloc(&s_tmem, 512);
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = s_tmem;
+
+    // A wait that gives up ends all later ones at once: the roles run out.
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (s_dead) return;
+        if (!mbar_wait(bar, parity)) {
+            s_dead = 1;
+            atomicOr(&L.ctrl->error, SPEC_WS_ERR_WAIT);
+        }
+    };
+    const uint32_t one2 = L.one2;
+
+    if (warp >= 8 && warp < kMmaWarp) {
+        // ---- codes to bf16 in shared memory: a token a thread ------------------
+        regs_down<kRegsDecode>();
+        const bool isv = warp >= 12;
+        const int t = tid & 127;
+        constexpr int kW = D / 8;               // words of a row's codes
+        uint32_t done = 0;                      // tiles of the whole share so far
+        for (long long pos = share.lo; pos < share.hi;) {
+            const Segment g = share.segment(pos);
+            pos = g.u_from + g.v1;
+            const Req<kTok> rq = share.rq;
+            // the first position that a row's window reaches (trees: the
+            // shallowest row's); what lies before may be anything
+            int low = rq.low;
+            if (A.window > 0 && A.depth) {
+                int least = A.n;
+                for (int i = lane; i < rq.rows; i += 32)
+                    least = min(least, max(A.depth[static_cast<long long>(g.b) * A.n + i], 0));
+                least = __reduce_min_sync(0xffffffffu, least);
+                low = max(0, rq.ctx + least - A.window + 1);
+            }
+            const unsigned char* head = A.pool.base + g.h * A.pool.head_stride + (isv ? Blk::v_codes(P) : 0);
+            // page of tile k's token, -1 where there is none or none is needed
+            auto page_of = [&](int k) {
+                if (k >= g.tiles) return -1;
+                const int at = rq.real(g.v0 + k) * kTok + t;
+                if (!rq.needs(A, at, at + 1) || (A.window > 0 && at < low && at >= A.sinks)) return -1;
+                const int page = cache_page(A.tab, A.pool.num_pages, p_shift, g.b, at);
+                if (page < 0 && !isv && A.status) atomicOr(A.status + g.b, SPEC_ST_BAD_PAGE);
+                return page;
+            };
+            struct Raw {
+                uint32_t w[kW];
+                uint32_t s[D / 64];
+            };
+            auto fetch = [&](Raw& r, int k, int page) {
+#pragma unroll
+                for (int i = 0; i < kW; ++i) r.w[i] = 0x88888888u;
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) r.s[i] = 0;
+                if (page < 0) return;
+                const int slot = (rq.real(g.v0 + k) * kTok + t) & (P - 1);
+                const unsigned char* blk = head + page * A.pool.page_stride;
+                const uint4* c = reinterpret_cast<const uint4*>(blk + slot * Blk::kRow);
+#pragma unroll
+                for (int i = 0; i < kW / 4; ++i) {
+                    const uint4 x = __ldg(c + i);
+                    r.w[4 * i] = x.x; r.w[4 * i + 1] = x.y; r.w[4 * i + 2] = x.z; r.w[4 * i + 3] = x.w;
+                }
+                const unsigned char* s = blk + P * Blk::kRow + slot * Blk::kScl;
+                if constexpr (D == 128) {
+                    const uint2 x = __ldg(reinterpret_cast<const uint2*>(s));
+                    r.s[0] = x.x; r.s[1] = x.y;
+                } else {
+                    r.s[0] = __ldg(reinterpret_cast<const uint32_t*>(s));
+                }
+            };
+            auto put = [&](const Raw& r) {
+                const int buf = done & 1;
+                wait(isv ? &bars.v_empty[buf] : &bars.k_empty[buf], ((done >> 1) & 1u) ^ 1u);
+                const uint32_t to = (isv ? v_buf : k_buf) + buf * kTile;
+#pragma unroll
+                for (int i = 0; i < kW; ++i) {
+                    const uint32_t s2 = __byte_perm(r.s[i >> 3], 0, (i >> 2) & 1 ? 0x3232 : 0x1010);
+                    const uint32_t c2 = minus1_5(s2);
+                    const uint32_t w = r.w[i];
+                    sts128(to + piece_at(t, i), codes2<0>(w, s2, c2, one2), codes2<1>(w, s2, c2, one2),
+                           codes2<2>(w, s2, c2, one2), codes2<3>(w, s2, c2, one2));
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(isv ? &bars.v_full[buf] : &bars.k_full[buf]);
+                ++done;
+            };
+            Raw a, z;
+            int p0 = page_of(0), p1 = page_of(1);
+            fetch(a, 0, p0);
+            for (int k = 0; k < g.tiles; k += 2) {
+                const int p2 = page_of(k + 2);
+                if (k + 1 < g.tiles) fetch(z, k + 1, p1);
+                put(a);
+                if (k + 1 >= g.tiles) break;
+                const int p3 = page_of(k + 3);
+                if (k + 2 < g.tiles) fetch(a, k + 2, p2);
+                put(z);
+                p1 = p3;
+            }
+        }
+    } else if (warp >= kMmaWarp) {
+        // ---- the tensor core's thread -----------------------------------------
+        regs_down<kRegsIssue>();
+        if (warp == kMmaWarp && lane == 0) {
+            constexpr uint32_t kQk = tc_idesc(128, false), kPv = tc_idesc(D, true);
+            uint32_t tiles_done = 0, segs = 0, p_seen[2] = {0, 0}, o_seen[2] = {0, 0};
+            for (long long pos = share.lo; pos < share.hi;) {
+                const Segment g = share.segment(pos);
+                pos = g.u_from + g.v1;
+                if (g.tiles == 0) continue;
+                const Req<kTok> rq = share.rq;
+                const int jobs = g.tiles * MT;
+                wait(&bars.q_full, segs & 1u);
+                ++segs;
+                auto qk = [&](int i) {
+                    const int k = i / MT, gr = i & 1;
+                    const uint32_t n = tiles_done + k, buf = n & 1;
+                    if (MT == 1 || gr == 0) wait(&bars.k_full[buf], (n >> 1) & 1u);
+                    tc_after();
+                    const uint32_t q = q_buf + (MT == 2 ? gr : 0) * Cfg::kQBytes, kb = k_buf + buf * kTile;
+                    if (!s_dead) {
+#pragma unroll
+                        for (int j = 0; j < D / 16; ++j) {
+                            const uint32_t at = (j >> 2) * kChunk + (j & 3) * 32;
+                            tc_mma(tmem + kS(gr), tc_desc(q + at), tc_desc(kb + at), kQk, j > 0);
+                        }
+                    }
+                    tc_commit(&bars.s_full[gr]);
+                    if (MT == 1 || gr == 1) tc_commit(&bars.k_empty[buf]);
+                    if (i == jobs - 1) tc_commit(&bars.q_empty);
+                };
+                auto pv = [&](int i) {
+                    const int k = i / MT, gr = i & 1;
+                    const uint32_t n = tiles_done + k, buf = n & 1;
+                    wait(&bars.p_full[gr], p_seen[gr]++ & 1u);
+                    if (MT == 1 || gr == 0) wait(&bars.v_full[buf], (n >> 1) & 1u);
+                    if (i < 2) {                // O is written anew: the last unit's has been read
+                        wait(&bars.o_free[gr], (o_seen[gr] & 1u) ^ 1u);
+                        ++o_seen[gr];
+                    }
+                    tc_after();
+                    const bool lo = rq.partial(A, rq.real(g.v0 + k) * kTok);
+                    const uint32_t vb = v_buf + buf * kTile;
+                    if (!s_dead) {
+#pragma unroll
+                        for (int j = 0; j < kTok / 16; ++j) {
+                            const uint32_t p = tmem + kS(gr) + 32 * (j >> 1) + 8 * (j & 1);
+                            const uint64_t vd = tc_desc(vb + j * 2048);
+                            tc_mma_ta(tmem + kO(gr), p, vd, kPv, i >= 2 || j > 0);
+                            if (lo) tc_mma_ta(tmem + kO(gr), p + 16, vd, kPv, 1);
+                        }
+                    }
+                    if (MT == 1 || gr == 1) tc_commit(&bars.v_empty[buf]);
+                    if (i + 2 >= jobs) tc_commit(&bars.o_done[gr]);
+                };
+                qk(0);
+                if (jobs > 1) qk(1);
+                for (int i = 0; i < jobs; ++i) {
+                    pv(i);
+                    if (i + 2 < jobs) qk(i + 2);
+                }
+                tiles_done += g.tiles;
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---- softmax: a row a thread -------------------------------------------
+        regs_up<kRegsSoftmax>();
+        const int gr = warp >> 2, r = tid & 127;
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;       // this warp's 32 lanes, in bits 16..
+        const uint32_t s_at = tmem + kS(gr) + lanes, o_at = tmem + kO(gr) + lanes;
+        const float cs = A.scale * kLog2e * 16.0f;
+        uint32_t segs = 0, s_seen = 0, o_seen = 0;
+        // Q's rows into shared memory: D/8 pieces of 8 a row, in the order of the
+        // decoded keys (elements 0 4 1 5 2 6 3 7)
+        auto load_q = [&](const Segment& g) {
+            wait(&bars.q_empty, (segs & 1u) ^ 1u);
+            ++segs;
+            const int row = (MT == 2 ? 128 * gr : 0) + r, rho = g.row0 + row;
+            const bool on = row < g.live_rows;
+            const int i = on ? static_cast<unsigned>(rho) / static_cast<unsigned>(A.G) : 0, gq = on ? rho - i * A.G : 0;
+            const uint16_t* q = A.q + g.b * A.q_bs + i * A.q_rs + (static_cast<long long>(g.h) * A.G + gq) * A.q_hs;
+            const int j0 = MT == 2 ? 0 : gr * (D / 16), j1 = MT == 2 ? D / 8 : j0 + D / 16;
+            const uint32_t to = q_buf + (MT == 2 ? gr : 0) * Cfg::kQBytes;
+#pragma unroll 8
+            for (int j = j0; j < j1; ++j) {
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (on) {
+                    if (A.aligned) {
+                        x = __ldg(reinterpret_cast<const uint4*>(q + 8 * j));
+                    } else {
+                        uint32_t y[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) y[e] = q[8 * j + 2 * e] | (static_cast<uint32_t>(q[8 * j + 2 * e + 1]) << 16);
+                        x = make_uint4(y[0], y[1], y[2], y[3]);
+                    }
+                }
+                sts128(to + piece_at(r, j), __byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
+                       __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.q_full);
+        };
+        Segment g = share.segment(share.lo);
+        if (g.tiles > 0) load_q(g);
+        for (;;) {
+            const Req<kTok> rq = share.rq;
+            const int row = (MT == 2 ? 128 * gr : 0) + r, rho = g.row0 + row;
+            const bool live = row < g.live_rows;
+            const bool warp_live = (row & ~31) < g.live_rows;
+            const int qi = static_cast<unsigned>(rho) / static_cast<unsigned>(A.G);     // the row's place among n
+            float m = kNoMax, l = 0.0f, lr = 0.0f;
+            const int k0 = MT == 2 ? 0 : gr;
+            for (int k = k0; k < g.tiles; k += MT == 2 ? 1 : 2) {
+                const int t0 = rq.real(g.v0 + k) * kTok;
+                // which of the tile's pages are there: a lane a page
+                bool absent = false;
+                const int pages = kTok >> p_shift;
+                if (lane < pages) {
+                    const int at = t0 + (lane << p_shift);
+                    absent = rq.needs(A, at, at + P) && cache_page(A.tab, A.pool.num_pages, p_shift, g.b, at) < 0;
+                }
+                const uint32_t gone = __ballot_sync(0xffffffffu, absent);
+                const bool lo = rq.partial(A, t0);
+                unsigned long long seen[2] = {~0ull, ~0ull};
+                if (warp_live && (lo || gone)) {
+                    seen[0] = live ? seen64(A, rq, g.b, qi, t0) : 0;
+                    seen[1] = live ? seen64(A, rq, g.b, qi, t0 + 64) : 0;
+                    for (uint32_t x = gone; x; x &= x - 1) {
+                        const int a = (__ffs(x) - 1) << p_shift;
+                        seen[a >> 6] &= ~range64(a & 63, (a & 63) + P, 0);
+                    }
+                }
+                wait(&bars.s_full[gr], s_seen++ & 1u);
+                tc_after();
+                if (warp_live) {
+                    auto tile = [&](auto is_masked) {
+                        constexpr bool kMasked = decltype(is_masked)::value;
+                        float x[32];
+                        auto load = [&](int c) {
+                            tc_ld32(x, s_at + 32 * c);
+                            tc_wait_ld();
+                            if constexpr (kMasked) {
+                                const uint32_t v = static_cast<uint32_t>(seen[c >> 1] >> (32 * (c & 1)));
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    if (!(v >> e & 1u)) x[e] = -CUDART_INF_F;
+                            }
+                        };
+                        float top = -CUDART_INF_F;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            load(c);
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2) top = fmaxf(top, fmaxf(x[e], x[e + 1]));
+                        }
+                        top *= cs;
+                        if (__any_sync(0xffffffffu, top > m + kSlack)) {
+                            const float mn = fmaxf(m, top), f = exp2_fast(m - mn);
+                            m = mn;
+                            l *= f;
+                            lr *= f;
+                            if (k > k0) {       // (the products of the tiles before are done: S came after them)
+#pragma unroll
+                                for (int c = 0; c < D / 32; ++c) {
+                                    tc_ld32(x, o_at + 32 * c);
+                                    tc_wait_ld();
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) x[e] *= f;
+                                    tc_st32(o_at + 32 * c, x);
+                                }
+                            }
+                        }
+                        // Weights, rounded to bf16 for the tensor core (2^-8 each at
+                        // most); lse takes their sum before that, the output is
+                        // divided by the sum of the rounded ones.  A tile where some
+                        // row does not see all adds a second term with what rounding
+                        // took from the first.
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            load(c);
+                            uint32_t hi[16], low[kMasked ? 16 : 1];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const float p0 = exp2_fast(fmaf(x[2 * e], cs, -m)), p1 = exp2_fast(fmaf(x[2 * e + 1], cs, -m));
+                                l += p0 + p1;
+                                hi[e] = pack_bf16(p0, p1);
+                                const float h0 = __uint_as_float(hi[e] << 16), h1 = __uint_as_float(hi[e] & 0xffff0000u);
+                                if constexpr (kMasked) {
+                                    low[e] = pack_bf16(p0 - h0, p1 - h1);
+                                    if (lo) lr += p0 + p1;
+                                    else lr += h0 + h1;
+                                } else {
+                                    lr += h0 + h1;
+                                }
+                            }
+                            tc_st16(s_at + 32 * c, hi);
+                            if constexpr (kMasked) tc_st16(s_at + 32 * c + 16, low);
+                        }
+                        tc_wait_st();
+                    };
+                    if (lo || gone) tile(std::true_type{});
+                    else tile(std::false_type{});
+                }
+                tc_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.p_full[gr]);
+            }
+
+            // ---- the next unit's Q, then this one's output ------------------------
+            const Segment cur = g;
+            const long long next = cur.u_from + cur.v1;
+            const bool more = next < share.hi;
+            if (more) {
+                g = share.segment(next);
+                if (g.tiles > 0) load_q(g);
+            }
+            const bool mine = MT == 2 ? cur.tiles > 0 : cur.tiles > k0;     // this group has an O
+            if (mine) {
+                wait(&bars.o_done[gr], o_seen++ & 1u);
+                tc_after();
+            }
+            const bool exists = rho < A.n * A.G;
+            const long long at_row = (static_cast<long long>(cur.b) * A.n + qi) * A.hq +
+                                     static_cast<long long>(cur.h) * A.G + (rho - qi * A.G);
+            const bool whole = cur.whole();
+            int c0 = blockIdx.x, parts = 1;
+            if (!whole) share.sharers(cur, c0, parts);
+            const int slot = 2 * static_cast<int>(blockIdx.x) + (c0 == static_cast<int>(blockIdx.x) ? 1 : 0);
+            const long long part_row = static_cast<long long>(slot) * Cfg::kRows + row;
+            // 32 columns of O, in the order of the decoded values, into the output
+            // or into the unit's parts
+            auto emit = [&](int c, const float (&v)[32], bool on, float f) {
+                uint4* to = reinterpret_cast<uint4*>(A.out + at_row * D + 32 * c);
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const float* y = v + 8 * w;
+                    uint4 u = make_uint4(0, 0, 0, 0);
+                    if (on)
+                        u = make_uint4(pack_bf16(y[0] * f, y[2] * f), pack_bf16(y[4] * f, y[6] * f),
+                                       pack_bf16(y[1] * f, y[3] * f), pack_bf16(y[5] * f, y[7] * f));
+                    to[w] = u;
+                }
+            };
+            auto finish = [&](int c, const float (&v)[32]) {
+                if (whole) {
+                    const bool on = live && l != 0.0f;
+                    if (exists) emit(c, v, on, on ? 16.0f / lr : 0.0f);
+                } else if (live) {
+                    float4* to = reinterpret_cast<float4*>(L.part + part_row * D + 32 * c);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) __stcg(to + e, make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]));
+                }
+            };
+            const bool any_here = (row & ~31) < cur.live_rows;
+            if constexpr (MT == 2) {
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    float v[32] = {};
+                    if (mine && any_here) {
+                        tc_ld32(v, o_at + 32 * c);
+                        tc_wait_ld();
+                    }
+                    finish(c, v);
+                }
+                tc_before();
+                __syncwarp();
+                if (mine && lane == 0) mbar_arrive(&bars.o_free[gr]);
+            } else {
+                // group 1's half is added to group 0's, 64 columns at a time
+                const uint32_t jrow = join + r * 256;
+                float f0 = 1.0f, f1 = 0.0f;
+                if (gr == 1) {
+                    s_join[r][0] = m;
+                    s_join[r][1] = l;
+                    s_join[r][2] = lr;
+                }
+#pragma unroll 1
+                for (int half = 0; half < D / 64; ++half) {
+                    if (gr == 1) {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            float v[32] = {};
+                            if (mine && any_here) {
+                                tc_ld32(v, o_at + 64 * half + 32 * c);
+                                tc_wait_ld();
+                            }
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                sts128(jrow + (((8 * c + e) ^ (r & 15)) << 4), __float_as_uint(v[4 * e]), __float_as_uint(v[4 * e + 1]),
+                                       __float_as_uint(v[4 * e + 2]), __float_as_uint(v[4 * e + 3]));
+                        }
+                    }
+                    asm volatile("bar.sync 3, 256;" ::: "memory");
+                    if (gr == 0) {
+                        if (half == 0) {
+                            const float m1 = s_join[r][0], mn = fmaxf(m, m1);
+                            f0 = exp2_fast(m - mn);
+                            f1 = exp2_fast(m1 - mn);
+                            m = mn;
+                            l = l * f0 + s_join[r][1] * f1;
+                            lr = lr * f0 + s_join[r][2] * f1;
+                        }
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            float v[32] = {};
+                            if (mine && any_here) {
+                                tc_ld32(v, o_at + 64 * half + 32 * c);
+                                tc_wait_ld();
+                            }
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                float4 y;
+                                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                             : "=f"(y.x), "=f"(y.y), "=f"(y.z), "=f"(y.w)
+                                             : "r"(jrow + (((8 * c + e) ^ (r & 15)) << 4)));
+                                v[4 * e] = v[4 * e] * f0 + y.x * f1;
+                                v[4 * e + 1] = v[4 * e + 1] * f0 + y.y * f1;
+                                v[4 * e + 2] = v[4 * e + 2] * f0 + y.z * f1;
+                                v[4 * e + 3] = v[4 * e + 3] * f0 + y.w * f1;
+                            }
+                            finish(2 * half + c, v);
+                        }
+                    }
+                    asm volatile("bar.sync 3, 256;" ::: "memory");
+                }
+                tc_before();
+                __syncwarp();
+                if (mine && lane == 0) mbar_arrive(&bars.o_free[gr]);
+            }
+            if (MT == 2 || gr == 0) {
+                if (whole) {
+                    if (exists && A.lse) A.lse[at_row] = live && l != 0.0f ? (m + log2f(l)) * kLn2 : -CUDART_INF_F;
+                } else {
+                    if (live) __stcg(reinterpret_cast<float4*>(L.ml) + part_row, make_float4(m, l, lr, 0.0f));
+                    __threadfence();
+                    group_sync(gr);
+                    if (r == 0) {
+                        uint32_t* count = &L.ctrl->arrived[2 * c0 + gr];
+                        const bool last = atomicAdd(count, 1u) == static_cast<uint32_t>(parts - 1);
+                        if (last) *count = 0;
+                        s_last[gr] = last;
+                    }
+                    group_sync(gr);
+                    if (s_last[gr]) {
+                        __threadfence();
+                        auto place = [&](int c) { return (2ll * (c0 + c) + (c == 0 ? 1 : 0)) * Cfg::kRows + row; };
+                        float mm = kNoMax, sum = 0.0f, rsum = 0.0f;
+                        if (live) {
+#pragma unroll 4
+                            for (int c = 0; c < parts; ++c) mm = fmaxf(mm, __ldcg(L.ml + place(c) * 4));
+#pragma unroll 4
+                            for (int c = 0; c < parts; ++c) {
+                                const float4 ml = __ldcg(reinterpret_cast<const float4*>(L.ml) + place(c));
+                                const float f = exp2_fast(ml.x - mm);
+                                sum += f * ml.y;
+                                rsum += f * ml.z;
+                            }
+                        }
+                        const bool on = live && sum != 0.0f;
+                        if (exists) {
+#pragma unroll 1
+                            for (int q = 0; q < D / 32; ++q) {
+                                float v[32] = {};
+                                if (live)
+                                    for (int c = 0; c < parts; ++c) {
+                                        const float f = exp2_fast(__ldcg(L.ml + place(c) * 4) - mm);
+                                        const float4* from = reinterpret_cast<const float4*>(L.part + place(c) * D + 32 * q);
+#pragma unroll
+                                        for (int e = 0; e < 8; ++e) {
+                                            const float4 y = __ldcg(from + e);
+                                            v[4 * e] += f * y.x;
+                                            v[4 * e + 1] += f * y.y;
+                                            v[4 * e + 2] += f * y.z;
+                                            v[4 * e + 3] += f * y.w;
+                                        }
+                                    }
+                                emit(q, v, on, on ? 16.0f / rsum : 0.0f);
+                            }
+                            if (A.lse) A.lse[at_row] = on ? (mm + log2f(sum)) * kLn2 : -CUDART_INF_F;
+                        }
+                    }
+                }
+            }
+            if (!more) break;
+        }
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    if (warp == kMmaWarp) tc_dealloc(tmem, 512);
+}
+
+template <int D, int MT>
+cudaError_t attend_tc(const CacheAttendArgs& A, cudaStream_t st) {
+    using Cfg = TcCfg<D, MT>;
+    const int grid = min(attend_sms(), kMaxGrid / 2);
+    const AttendLayout y(2 * grid, Cfg::kRows, D);
+    AttendPlan L;
+    L.one2 = 0x3F803F80u;
+    L.grid = grid;
+    L.row_tiles = (A.n * A.G + Cfg::kRows - 1) / Cfg::kRows;
+    L.min_tiles = 2;
+    const long long tiles = ((static_cast<long long>(A.tab.width) << A.pool.p_shift) + A.n) / kTok + 2;
+    if (tiles * A.pool.heads * L.row_tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
+    unsigned char* ws = static_cast<unsigned char*>(A.ws);
+    L.ctrl = reinterpret_cast<AttendCtrl*>(ws);
+    L.ml = reinterpret_cast<float*>(ws + y.ml);
+    L.part = reinterpret_cast<float*>(ws + y.part);
+    static std::atomic<unsigned long long> ready{0};
+    const int dev = attend_device();
+    if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+        const cudaError_t e = cudaFuncSetAttribute(cache_attend_tc_kernel<D, MT>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
+    cache_attend_tc_kernel<D, MT><<<grid, kThreads, Cfg::kSmem, st>>>(A, L);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t attend_tc_ws(int R, int D) {
+    return AttendLayout(2 * min(attend_sms(), kMaxGrid / 2), R <= 128 ? 128 : 256, D).bytes;
+}
+
+cudaError_t attend_tc_run(const CacheAttendArgs& A, cudaStream_t st) {
+    const bool one = A.n * A.G <= 128;
+    if (A.pool.D == 128) return one ? attend_tc<128, 1>(A, st) : attend_tc<128, 2>(A, st);
+    return one ? attend_tc<64, 1>(A, st) : attend_tc<64, 2>(A, st);
+}
+
+}  // namespace spec
