@@ -33,7 +33,7 @@ namespace {
 constexpr int kAtWarps = 4;
 constexpr int kAtThreads = 32 * kAtWarps;
 constexpr int kTile = 64;                       // tokens a tile
-constexpr int kFewRows = 16;                    // rows a kv head that this kernel takes
+constexpr int kFewRows = 96;                    // rows a kv head that this kernel takes
 
 __device__ __forceinline__ uint32_t lds16(uint32_t a) {
     unsigned short v;
@@ -137,7 +137,7 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
     }
 
     Share<kTile, kAtWarps> share(A, L, s_share, kRows);
-    if (share.lo == share.hi) return;
+    if (share.lo() == share.hi()) return;
     const int cta = blockIdx.x;
 
     uint32_t phases = 0;                        // one bit a stage
@@ -213,7 +213,7 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
         }
     };
 
-    Segment g = share.segment(share.lo);
+    Segment g = share.segment(share.lo());
     begin(g);
     for (;;) {
         // ---- Q, laid out like the keys' words -------------------------------
@@ -495,7 +495,7 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
         __syncthreads();
         // every warp is past its last tile: the next segment may begin
         const Segment cur = g;
-        const bool more = cur.u_from + cur.v1 < share.hi;
+        const bool more = cur.u_from + cur.v1 < share.hi();
         if (more) {
             g = share.segment(cur.u_from + cur.v1);
             begin(g);
@@ -702,7 +702,7 @@ cudaError_t attend_rows(const CacheAttendArgs& A, cudaStream_t st) {
 size_t cache_attend_ws(int B, int n, int hq, int hkv, int D) {
     (void)B;
     const int R = n * (hq / hkv);
-    if (R > kFewRows) return attend_tc_ws(R, D);
+    if (R > kFewRows) return attend_tc_ws(D);
     const int NT = row_blocks(R);
     return AttendLayout(2 * min(attend_sms() * ctas_of(NT), kMaxGrid), 8 * NT, D).bytes;
 }

@@ -105,6 +105,8 @@ struct Segment {
 template <int kWarps>
 struct ShareScratch {                           // in shared memory
     long long sum[kWarps], found[2];
+    long long total, lo, hi;                    // all tiles, and this CTA's share of them
+    int active;                                 // CTAs that have work
     int2 len[32 * kWarps];                      // the first requests' lengths
 };
 
@@ -115,8 +117,10 @@ struct Share {
     const AttendPlan& L;
     const ShareScratch<kWarps>& S;
     const int rows_a_block;
-    long long total, lo, hi;
-    int active;                                 // CTAs that have work
+    // the share's limits: in registers where the CTA is small, else in shared memory
+    static constexpr bool kRegs = kWarps <= 4;
+    long long total_, lo_, hi_;
+    int active_;
     int b;                                      // the cursor's request, and where its tiles start
     long long b_from;
     Req<kTile> rq;
@@ -125,10 +129,10 @@ struct Share {
     static __device__ __forceinline__ long long quotient(long long x, long long y) {
         return (x | y) >> 32 ? x / y : static_cast<long long>(static_cast<unsigned>(x) / static_cast<unsigned>(y));
     }
-    __device__ __forceinline__ long long start_of(long long c) const { return quotient(c * total, active); }
+    __device__ __forceinline__ long long start_of(long long c) const { return quotient(c * total(), active()); }
     // the CTA whose share holds tile x
     __device__ __forceinline__ int cta_of(long long x) const {
-        int c = static_cast<int>(quotient(x * active, total));
+        int c = static_cast<int>(quotient(x * active(), total()));
         while (start_of(c + 1) <= x) ++c;
         while (start_of(c) > x) --c;
         return c;
@@ -136,6 +140,11 @@ struct Share {
     __device__ __forceinline__ Req<kTile> req_at(int i) const {
         return Req<kTile>(A, i < 32 * kWarps ? S.len[i] : request_len(A, i));
     }
+
+    __device__ __forceinline__ long long total() const { return kRegs ? total_ : S.total; }
+    __device__ __forceinline__ long long lo() const { return kRegs ? lo_ : S.lo; }
+    __device__ __forceinline__ long long hi() const { return kRegs ? hi_ : S.hi; }
+    __device__ __forceinline__ int active() const { return kRegs ? active_ : S.active; }
 
     // Every thread of the CTA takes part.  A CTA without work has lo == hi.
     __device__ __forceinline__ Share(const CacheAttendArgs& A_, const AttendPlan& L_, ShareScratch<kWarps>& scratch,
@@ -151,8 +160,7 @@ struct Share {
             return static_cast<long long>(H) * Req<kTile>(A, given).head_work(A, L.row_tiles, rows_a_block);
         };
         // the requests a chunk of threads at a time; one chunk is the usual case
-        long long first_work = 0;
-        total = 0;
+        long long first_work = 0, total = 0;            // (total: as the member, while it is counted)
         for (int b0 = 0; b0 < A.B; b0 += kThreads) {
             const long long v = work_of(b0 + tid);
             if (b0 == 0) {
@@ -171,15 +179,25 @@ struct Share {
         const long long units = static_cast<long long>(A.B) * H * L.row_tiles;
         long long want = quotient(total, L.min_tiles);
         if (want > units * 64) want = units * 64;           // what joins a unit must stay small beside it
-        active = static_cast<int>(min(static_cast<long long>(gridDim.x), max(want, 1ll)));
+        const int active = static_cast<int>(min(static_cast<long long>(gridDim.x), max(want, 1ll)));
         const int cta = blockIdx.x;
-        lo = hi = 0;
         b = 0;
         b_from = 0;
-        if (cta >= active) return;
-        lo = start_of(cta);
-        hi = start_of(cta + 1);
+        const long long lo = cta < active ? quotient(cta * total, active) : 0;
+        const long long hi = cta < active ? quotient((cta + 1) * total, active) : 0;
+        if constexpr (kRegs) {
+            total_ = total;
+            active_ = active;
+            lo_ = lo;
+            hi_ = hi;
+        } else if (tid == 0) {
+            scratch.total = total;
+            scratch.active = active;
+            scratch.lo = lo;
+            scratch.hi = hi;
+        }
         __syncthreads();
+        if (cta >= active) return;
         // the request that holds tile lo, and where its tiles start
         long long before = 0;
         for (int b0 = 0; b0 < A.B; b0 += kThreads) {
@@ -239,7 +257,7 @@ struct Share {
             g.v0 = 0;
         }
         g.u_from = pos - g.v0;
-        g.v1 = static_cast<int>(min(static_cast<long long>(g.tiles_u), hi - g.u_from));
+        g.v1 = static_cast<int>(min(static_cast<long long>(g.tiles_u), hi() - g.u_from));
         g.row0 = rt * rows_a_block;
         g.live_rows = min(max(rq.rows * A.G - g.row0, 0), rows_a_block);
         g.tiles = g.live_rows > 0 ? g.v1 - g.v0 : 0;
@@ -350,7 +368,7 @@ struct AttendLayout {
 };
 
 // many rows a kv head: tcgen05 (spec_cache_attend_tc.cu)
-size_t attend_tc_ws(int R, int D);
+size_t attend_tc_ws(int D);
 cudaError_t attend_tc_run(const CacheAttendArgs& A, cudaStream_t st);
 
 }  // namespace spec

@@ -16,15 +16,13 @@
 //                memory (128-byte swizzle); warps 12-15 the same for the values;
 //   warp 16      one thread issues the tensor work: S_g = Q K^T (both in shared
 //                memory) and O_g += P_g V with P_g in tensor memory where S_g was;
-//   warps 0-3, 4-7  two softmax groups, g = 0 and 1, each with its own S, P, O in
-//                tensor memory, so that one group's exponentials run beside the
-//                other's products.  With up to 128 rows (MT = 1) the groups take
-//                alternate tiles and their halves are joined at a unit's end; with
-//                more (MT = 2) each takes 128 of the rows and they share a tile's
-//                decoded keys and values.
-// What bounds it, a tile of 128 tokens: shared memory, 64 KB written and 96 KB
-// (MT = 1) or 192 KB read by the tensor core at 128 bytes a cycle; the tensor core
-// itself, 1024 or 2048 cycles at D = 128.
+//   warps 0-3, 4-7  two softmax groups, g = 0 and 1, with 128 of a unit's 256 rows
+//                each and their own S, P, O in tensor memory, so that one group's
+//                exponentials run beside the other's products.  A unit of up to 128
+//                rows is group 0's alone; its tiles take the two S in turn.
+// What bounds it, a tile of 128 tokens: shared memory, 64 KB written and 192 KB
+// read by the tensor core at 128 bytes a cycle; the tensor core itself, 2048 cycles
+// at D = 128.
 #include <atomic>
 #include <type_traits>
 
@@ -39,18 +37,18 @@ constexpr int kWarps = 20;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMmaWarp = 16;
 // Registers a thread: 96 at launch (640 threads), then moved from the decoders and
-// the issuing group to the softmax: 256 * 80 + 128 * 56 + 256 * 128 = 60416 of the
+// the issuing group to the softmax: 256 * 72 + 128 * 72 + 256 * 128 = 60416 of the
 // 61440 that the block was launched with.
-constexpr int kRegsDecode = 80, kRegsIssue = 56, kRegsSoftmax = 128;
+constexpr int kRegsDecode = 72, kRegsIssue = 72, kRegsSoftmax = 128;
 static_assert(256 * kRegsDecode + 128 * kRegsIssue + 256 * kRegsSoftmax <= 96 * kThreads, "register shares");
 
-template <int D, int MT>
+constexpr int kRows = 256;                      // rows a unit
+
+template <int D>
 struct TcCfg {
-    static constexpr int kRows = 128 * MT;
     static constexpr int kTileBytes = kTok * D * 2;         // a tile's keys or values in bf16
     static constexpr int kQBytes = 128 * D * 2;             // 128 rows of Q
-    static constexpr int kJoin = MT == 1 ? 128 * 64 * 4 : 0;    // half a block of O, where groups are joined
-    static constexpr int kSmem = 4 * kTileBytes + MT * kQBytes + kJoin + 1024;
+    static constexpr int kSmem = 4 * kTileBytes + 2 * kQBytes + 1024;
 };
 
 // tensor memory, in columns: S (P) of the groups, then O
@@ -100,17 +98,19 @@ __device__ __forceinline__ void tc_ld32(float (&x)[32], uint32_t at) {
           "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(at));
 }
-__device__ __forceinline__ void tc_st32(uint32_t at, const float (&x)[32]) {
-    const uint32_t* r = reinterpret_cast<const uint32_t*>(x);
+__device__ __forceinline__ void tc_ld16(float (&x)[16], uint32_t at) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(x);
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
-        :: "r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-           "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-           "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
-           "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(at));
+}
+__device__ __forceinline__ void tc_st8(uint32_t at, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 :: "r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 __device__ __forceinline__ void tc_st16(uint32_t at, const uint32_t (&r)[16]) {
     asm volatile(
@@ -138,6 +138,22 @@ constexpr int kChunk = 16384;                   // bytes of 64 columns of 128 ro
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
+// two fp32 operations in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<unsigned long long&>(r))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+          "l"(reinterpret_cast<unsigned long long&>(c)));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long&>(r))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+    return r;
+}
 // where piece j (8 elements, 16 bytes) of row r lies in such a matrix
 __device__ __forceinline__ uint32_t piece_at(int r, int j) {
     return (j >> 3) * kChunk + r * 128 + (((j & 7) ^ (r & 7)) << 4);
@@ -156,14 +172,15 @@ __device__ __forceinline__ void group_sync(int g) {
 // ---------------------------------------------------------------------------
 struct TcBars {
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];      // a tile's keys, values
-    uint64_t s_full[2], p_full[2], o_done[2], o_free[2];        // by group
-    uint64_t q_full, q_empty;
+    uint64_t s_full[2], p_full[2];              // by S
+    uint64_t o_done[2], o_free[2];              // by group: a unit's last product, its O read
+    uint64_t q_full, q_empty, pv_done;
 };
 
-template <int D, int MT>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_constant__ AttendPlan L) {
-    using Cfg = TcCfg<D, MT>;
+    using Cfg = TcCfg<D>;
     using Blk = CacheBlock<D>;
     constexpr int kTile = Cfg::kTileBytes;
     extern __shared__ unsigned char smem_raw[];
@@ -172,16 +189,15 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_dead;
     __shared__ int s_last[2];
-    __shared__ float s_join[MT == 1 ? 128 : 1][3];
 
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int P = A.pool.P, p_shift = A.pool.p_shift;
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t v_buf = base, k_buf = base + 2 * kTile, q_buf = base + 4 * kTile, join = q_buf + MT * Cfg::kQBytes;
+    const uint32_t v_buf = base, k_buf = base + 2 * kTile, q_buf = base + 4 * kTile;
 
-    Share<kTok, kWarps> share(A, L, s_share, Cfg::kRows);
-    if (share.lo == share.hi) return;
+    Share<kTok, kWarps> share(A, L, s_share, kRows);
+    if (share.lo() == share.hi()) return;
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars.k_full[i], 4);
@@ -195,6 +211,7 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
         }
         mbar_init(&bars.q_full, 8);
         mbar_init(&bars.q_empty, 1);
+        mbar_init(&bars.pv_done, 1);
         fence_mbar_init();
         s_dead = 0;
     }
@@ -221,7 +238,7 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
         const int t = tid & 127;
         constexpr int kW = D / 8;               // words of a row's codes
         uint32_t done = 0;                      // tiles of the whole share so far
-        for (long long pos = share.lo; pos < share.hi;) {
+        for (long long pos = share.lo(); pos < share.hi();) {
             const Segment g = share.segment(pos);
             pos = g.u_from + g.v1;
             const Req<kTok> rq = share.rq;
@@ -236,14 +253,28 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
                 low = max(0, rq.ctx + least - A.window + 1);
             }
             const unsigned char* head = A.pool.base + g.h * A.pool.head_stride + (isv ? Blk::v_codes(P) : 0);
-            // page of tile k's token, -1 where there is none or none is needed
-            auto page_of = [&](int k) {
-                if (k >= g.tiles) return -1;
+            // The page of tile k's token: looked up (load_page) two tiles ahead and
+            // judged (page_of) only when the codes are fetched, so that nothing waits
+            // for the table.
+            struct Page {
+                int id;
+                bool wanted;
+            };
+            auto load_page = [&](int k) {
+                Page p;
+                p.wanted = false;
+                p.id = -1;
+                if (k >= g.tiles) return p;
                 const int at = rq.real(g.v0 + k) * kTok + t;
-                if (!rq.needs(A, at, at + 1) || (A.window > 0 && at < low && at >= A.sinks)) return -1;
-                const int page = cache_page(A.tab, A.pool.num_pages, p_shift, g.b, at);
-                if (page < 0 && !isv && A.status) atomicOr(A.status + g.b, SPEC_ST_BAD_PAGE);
-                return page;
+                p.wanted = rq.needs(A, at, at + 1) && !(A.window > 0 && at < low && at >= A.sinks);
+                if (p.wanted && (at >> p_shift) < A.tab.width)
+                    p.id = static_cast<int>(ldg_now_u32(A.tab.table + g.b * A.tab.stride + (at >> p_shift)));
+                return p;
+            };
+            auto page_of = [&](const Page& p) {
+                const bool there = static_cast<unsigned>(p.id) < static_cast<unsigned>(A.pool.num_pages);
+                if (p.wanted && !there && !isv && A.status) atomicOr(A.status + g.b, SPEC_ST_BAD_PAGE);
+                return there ? p.id : -1;
             };
             struct Raw {
                 uint32_t w[kW];
@@ -289,17 +320,16 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
                 ++done;
             };
             Raw a, z;
-            int p0 = page_of(0), p1 = page_of(1);
-            fetch(a, 0, p0);
+            Page p0 = load_page(0), p1 = load_page(1);
+            fetch(a, 0, page_of(p0));
             for (int k = 0; k < g.tiles; k += 2) {
-                const int p2 = page_of(k + 2);
-                if (k + 1 < g.tiles) fetch(z, k + 1, p1);
+                p0 = load_page(k + 2);
+                if (k + 1 < g.tiles) fetch(z, k + 1, page_of(p1));
                 put(a);
                 if (k + 1 >= g.tiles) break;
-                const int p3 = page_of(k + 3);
-                if (k + 2 < g.tiles) fetch(a, k + 2, p2);
+                p1 = load_page(k + 3);
+                if (k + 2 < g.tiles) fetch(a, k + 2, page_of(p0));
                 put(z);
-                p1 = p3;
             }
         }
     } else if (warp >= kMmaWarp) {
@@ -308,20 +338,23 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
         if (warp == kMmaWarp && lane == 0) {
             constexpr uint32_t kQk = tc_idesc(128, false), kPv = tc_idesc(D, true);
             uint32_t tiles_done = 0, segs = 0, p_seen[2] = {0, 0}, o_seen[2] = {0, 0};
-            for (long long pos = share.lo; pos < share.hi;) {
+            for (long long pos = share.lo(); pos < share.hi();) {
                 const Segment g = share.segment(pos);
                 pos = g.u_from + g.v1;
                 if (g.tiles == 0) continue;
                 const Req<kTok> rq = share.rq;
-                const int jobs = g.tiles * MT;
+                // a job is a tile of 128 rows; it takes S i & 1, the group's with two
+                // groups, else in turn
+                const bool two = g.live_rows > 128;
+                const int jobs = two ? 2 * g.tiles : g.tiles;
                 wait(&bars.q_full, segs & 1u);
                 ++segs;
                 auto qk = [&](int i) {
-                    const int k = i / MT, gr = i & 1;
-                    const uint32_t n = tiles_done + k, buf = n & 1;
-                    if (MT == 1 || gr == 0) wait(&bars.k_full[buf], (n >> 1) & 1u);
+                    const int gr = i & 1;
+                    const uint32_t n = tiles_done + (two ? i >> 1 : i), buf = n & 1;
+                    if (!two || gr == 0) wait(&bars.k_full[buf], (n >> 1) & 1u);
                     tc_after();
-                    const uint32_t q = q_buf + (MT == 2 ? gr : 0) * Cfg::kQBytes, kb = k_buf + buf * kTile;
+                    const uint32_t q = q_buf + (two ? gr : 0) * Cfg::kQBytes, kb = k_buf + buf * kTile;
                     if (!s_dead) {
 #pragma unroll
                         for (int j = 0; j < D / 16; ++j) {
@@ -330,15 +363,16 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
                         }
                     }
                     tc_commit(&bars.s_full[gr]);
-                    if (MT == 1 || gr == 1) tc_commit(&bars.k_empty[buf]);
+                    if (!two || gr == 1) tc_commit(&bars.k_empty[buf]);
                     if (i == jobs - 1) tc_commit(&bars.q_empty);
                 };
                 auto pv = [&](int i) {
-                    const int k = i / MT, gr = i & 1;
+                    const int sb = i & 1, gr = two ? sb : 0, k = two ? i >> 1 : i;
                     const uint32_t n = tiles_done + k, buf = n & 1;
-                    wait(&bars.p_full[gr], p_seen[gr]++ & 1u);
-                    if (MT == 1 || gr == 0) wait(&bars.v_full[buf], (n >> 1) & 1u);
-                    if (i < 2) {                // O is written anew: the last unit's has been read
+                    const bool first = k == 0, last = k == g.tiles - 1;
+                    wait(&bars.p_full[sb], p_seen[sb]++ & 1u);
+                    if (gr == 0) wait(&bars.v_full[buf], (n >> 1) & 1u);
+                    if (first) {                // O is written anew: the last unit's has been read
                         wait(&bars.o_free[gr], (o_seen[gr] & 1u) ^ 1u);
                         ++o_seen[gr];
                     }
@@ -348,14 +382,15 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
                     if (!s_dead) {
 #pragma unroll
                         for (int j = 0; j < kTok / 16; ++j) {
-                            const uint32_t p = tmem + kS(gr) + 32 * (j >> 1) + 8 * (j & 1);
+                            const uint32_t p = tmem + kS(sb) + 32 * (j >> 1) + 8 * (j & 1);
                             const uint64_t vd = tc_desc(vb + j * 2048);
-                            tc_mma_ta(tmem + kO(gr), p, vd, kPv, i >= 2 || j > 0);
+                            tc_mma_ta(tmem + kO(gr), p, vd, kPv, !first || j > 0);
                             if (lo) tc_mma_ta(tmem + kO(gr), p + 16, vd, kPv, 1);
                         }
                     }
-                    if (MT == 1 || gr == 1) tc_commit(&bars.v_empty[buf]);
-                    if (i + 2 >= jobs) tc_commit(&bars.o_done[gr]);
+                    if (!two) tc_commit(&bars.pv_done);
+                    if (!two || gr == 1) tc_commit(&bars.v_empty[buf]);
+                    if (last) tc_commit(&bars.o_done[gr]);
                 };
                 qk(0);
                 if (jobs > 1) qk(1);
@@ -372,24 +407,24 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
         regs_up<kRegsSoftmax>();
         const int gr = warp >> 2, r = tid & 127;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;       // this warp's 32 lanes, in bits 16..
-        const uint32_t s_at = tmem + kS(gr) + lanes, o_at = tmem + kO(gr) + lanes;
+        const uint32_t o_at = tmem + kO(gr) + lanes;
         const float cs = A.scale * kLog2e * 16.0f;
-        uint32_t segs = 0, s_seen = 0, o_seen = 0;
+        uint32_t segs = 0, o_seen = 0, pv_seen = 0;
+        uint32_t s_seen[2] = {0, 0};            // (both groups count both S)
         // Q's rows into shared memory: D/8 pieces of 8 a row, in the order of the
         // decoded keys (elements 0 4 1 5 2 6 3 7)
         auto load_q = [&](const Segment& g) {
             wait(&bars.q_empty, (segs & 1u) ^ 1u);
             ++segs;
-            const int row = (MT == 2 ? 128 * gr : 0) + r, rho = g.row0 + row;
+            const int row = 128 * gr + r, rho = g.row0 + row;
             const bool on = row < g.live_rows;
             const int i = on ? static_cast<unsigned>(rho) / static_cast<unsigned>(A.G) : 0, gq = on ? rho - i * A.G : 0;
             const uint16_t* q = A.q + g.b * A.q_bs + i * A.q_rs + (static_cast<long long>(g.h) * A.G + gq) * A.q_hs;
-            const int j0 = MT == 2 ? 0 : gr * (D / 16), j1 = MT == 2 ? D / 8 : j0 + D / 16;
-            const uint32_t to = q_buf + (MT == 2 ? gr : 0) * Cfg::kQBytes;
+            const uint32_t to = q_buf + gr * Cfg::kQBytes;
+            if (on) {
 #pragma unroll 8
-            for (int j = j0; j < j1; ++j) {
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (on) {
+                for (int j = 0; j < D / 8; ++j) {
+                    uint4 x;
                     if (A.aligned) {
                         x = __ldg(reinterpret_cast<const uint4*>(q + 8 * j));
                     } else {
@@ -398,81 +433,110 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
                         for (int e = 0; e < 4; ++e) y[e] = q[8 * j + 2 * e] | (static_cast<uint32_t>(q[8 * j + 2 * e + 1]) << 16);
                         x = make_uint4(y[0], y[1], y[2], y[3]);
                     }
+                    sts128(to + piece_at(r, j), __byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
+                           __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
                 }
-                sts128(to + piece_at(r, j), __byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
-                       __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.q_full);
         };
-        Segment g = share.segment(share.lo);
+        Segment g = share.segment(share.lo());
         if (g.tiles > 0) load_q(g);
         for (;;) {
             const Req<kTok> rq = share.rq;
-            const int row = (MT == 2 ? 128 * gr : 0) + r, rho = g.row0 + row;
+            const int row = 128 * gr + r, rho = g.row0 + row;
             const bool live = row < g.live_rows;
-            const bool warp_live = (row & ~31) < g.live_rows;
+            const bool warp_live = (row & ~31) < g.live_rows, two = g.live_rows > 128;
             const int qi = static_cast<unsigned>(rho) / static_cast<unsigned>(A.G);     // the row's place among n
-            float m = kNoMax, l = 0.0f, lr = 0.0f;
-            const int k0 = MT == 2 ? 0 : gr;
-            for (int k = k0; k < g.tiles; k += MT == 2 ? 1 : 2) {
+            float m = kNoMax;
+            float2 l2 = make_float2(0.0f, 0.0f), lr2 = l2;      // two partial sums each
+            const int mine = two || gr == 0 ? g.tiles : 0;      // this group's tiles
+            // which of a tile's pages are missing: a lane a page, looked up a tile
+            // ahead and judged when its turn comes
+            int page = 0;
+            auto look_up = [&](int k) {
+                page = 0;
+                if (k >= mine || lane >= kTok >> p_shift) return;
+                const int at = rq.real(g.v0 + k) * kTok + (lane << p_shift);
+                if (rq.needs(A, at, at + P))
+                    page = (at >> p_shift) < A.tab.width
+                               ? static_cast<int>(ldg_now_u32(A.tab.table + g.b * A.tab.stride + (at >> p_shift)))
+                               : -1;
+            };
+            look_up(0);
+            for (int k = 0; k < mine; ++k) {
+                const int sb = two ? gr : k & 1;
+                const uint32_t s_at = tmem + kS(sb) + lanes;
                 const int t0 = rq.real(g.v0 + k) * kTok;
-                // which of the tile's pages are there: a lane a page
-                bool absent = false;
-                const int pages = kTok >> p_shift;
-                if (lane < pages) {
-                    const int at = t0 + (lane << p_shift);
-                    absent = rq.needs(A, at, at + P) && cache_page(A.tab, A.pool.num_pages, p_shift, g.b, at) < 0;
-                }
-                const uint32_t gone = __ballot_sync(0xffffffffu, absent);
+                const uint32_t gone =
+                    __ballot_sync(0xffffffffu, static_cast<unsigned>(page) >= static_cast<unsigned>(A.pool.num_pages));
+                look_up(k + 1);
                 const bool lo = rq.partial(A, t0);
-                unsigned long long seen[2] = {~0ull, ~0ull};
+                unsigned long long seen0 = ~0ull, seen1 = ~0ull;
                 if (warp_live && (lo || gone)) {
-                    seen[0] = live ? seen64(A, rq, g.b, qi, t0) : 0;
-                    seen[1] = live ? seen64(A, rq, g.b, qi, t0 + 64) : 0;
+                    seen0 = live ? seen64(A, rq, g.b, qi, t0) : 0;
+                    seen1 = live ? seen64(A, rq, g.b, qi, t0 + 64) : 0;
+#pragma unroll 1
                     for (uint32_t x = gone; x; x &= x - 1) {
                         const int a = (__ffs(x) - 1) << p_shift;
-                        seen[a >> 6] &= ~range64(a & 63, (a & 63) + P, 0);
+                        const unsigned long long off = range64(a & 63, (a & 63) + P, 0);
+                        if (a < 64) seen0 &= ~off;
+                        else seen1 &= ~off;
                     }
                 }
-                wait(&bars.s_full[gr], s_seen++ & 1u);
+                wait(&bars.s_full[sb], ((sb ? s_seen[1] : s_seen[0]) + (two ? k : k >> 1)) & 1u);
                 tc_after();
                 if (warp_live) {
                     auto tile = [&](auto is_masked) {
                         constexpr bool kMasked = decltype(is_masked)::value;
-                        float x[32];
-                        auto load = [&](int c) {
-                            tc_ld32(x, s_at + 32 * c);
-                            tc_wait_ld();
+                        // 16 columns at a time, the next on their way
+                        float x[16], y[16];
+                        auto mask = [&](float (&z)[16], int c) {
                             if constexpr (kMasked) {
-                                const uint32_t v = static_cast<uint32_t>(seen[c >> 1] >> (32 * (c & 1)));
+                                const uint32_t v = static_cast<uint32_t>((c >> 2 ? seen1 : seen0) >> (16 * (c & 3)));
 #pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    if (!(v >> e & 1u)) x[e] = -CUDART_INF_F;
+                                for (int e = 0; e < 16; ++e)
+                                    if (!(v >> e & 1u)) z[e] = -CUDART_INF_F;
                             }
                         };
                         float top = -CUDART_INF_F;
+                        auto look = [&](float (&z)[16], int c) {
+                            mask(z, c);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            load(c);
-#pragma unroll
-                            for (int e = 0; e < 32; e += 2) top = fmaxf(top, fmaxf(x[e], x[e + 1]));
+                            for (int e = 0; e < 16; e += 2) top = fmaxf(top, fmaxf(z[e], z[e + 1]));
+                        };
+                        tc_ld16(x, s_at);
+#pragma unroll 1
+                        for (int c = 0; c < 8; c += 2) {
+                            tc_wait_ld();
+                            tc_ld16(y, s_at + 16 * (c + 1));
+                            look(x, c);
+                            tc_wait_ld();
+                            tc_ld16(x, s_at + 16 * ((c + 2) & 7));      // (the last: the first again)
+                            look(y, c + 1);
                         }
                         top *= cs;
                         if (__any_sync(0xffffffffu, top > m + kSlack)) {
                             const float mn = fmaxf(m, top), f = exp2_fast(m - mn);
                             m = mn;
-                            l *= f;
-                            lr *= f;
-                            if (k > k0) {       // (the products of the tiles before are done: S came after them)
-#pragma unroll
-                                for (int c = 0; c < D / 32; ++c) {
-                                    tc_ld32(x, o_at + 32 * c);
+                            l2 = make_float2(l2.x * f, l2.y * f);
+                            lr2 = make_float2(lr2.x * f, lr2.y * f);
+                            if (k > 0) {
+                                // the products so far must be done: with two groups S
+                                // came after the group's last
+                                if (!two) {
+                                    wait(&bars.pv_done, (pv_seen + k - 1) & 1u);
+                                    tc_after();
+                                }
+#pragma unroll 1
+                                for (int c = 0; c < D / 16; ++c) {
+                                    tc_ld16(y, o_at + 16 * c);
                                     tc_wait_ld();
+                                    uint32_t u[16];
 #pragma unroll
-                                    for (int e = 0; e < 32; ++e) x[e] *= f;
-                                    tc_st32(o_at + 32 * c, x);
+                                    for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(y[e] * f);
+                                    tc_st16(o_at + 16 * c, u);
                                 }
                             }
                         }
@@ -481,26 +545,37 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
                         // divided by the sum of the rounded ones.  A tile where some
                         // row does not see all adds a second term with what rounding
                         // took from the first.
+                        const float2 cs2 = make_float2(cs, cs), m2 = make_float2(-m, -m);
+                        auto weigh = [&](float (&z)[16], int c) {
+                            mask(z, c);
+                            uint32_t hi[8], low[kMasked ? 8 : 1];
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            load(c);
-                            uint32_t hi[16], low[kMasked ? 16 : 1];
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const float p0 = exp2_fast(fmaf(x[2 * e], cs, -m)), p1 = exp2_fast(fmaf(x[2 * e + 1], cs, -m));
-                                l += p0 + p1;
-                                hi[e] = pack_bf16(p0, p1);
-                                const float h0 = __uint_as_float(hi[e] << 16), h1 = __uint_as_float(hi[e] & 0xffff0000u);
+                            for (int e = 0; e < 8; ++e) {
+                                const float2 a = fma2(make_float2(z[2 * e], z[2 * e + 1]), cs2, m2);
+                                const float2 p = make_float2(exp2_fast(a.x), exp2_fast(a.y));
+                                l2 = add2(l2, p);
+                                hi[e] = pack_bf16(p.x, p.y);
+                                const float2 h = make_float2(__uint_as_float(hi[e] << 16), __uint_as_float(hi[e] & 0xffff0000u));
                                 if constexpr (kMasked) {
-                                    low[e] = pack_bf16(p0 - h0, p1 - h1);
-                                    if (lo) lr += p0 + p1;
-                                    else lr += h0 + h1;
+                                    low[e] = pack_bf16(p.x - h.x, p.y - h.y);
+                                    lr2 = add2(lr2, lo ? p : h);
                                 } else {
-                                    lr += h0 + h1;
+                                    lr2 = add2(lr2, h);
                                 }
                             }
-                            tc_st16(s_at + 32 * c, hi);
-                            if constexpr (kMasked) tc_st16(s_at + 32 * c + 16, low);
+                            // P's 32 columns of S: 16 of weights, 16 of second terms
+                            const uint32_t to = s_at + 32 * (c >> 1) + 8 * (c & 1);
+                            tc_st8(to, hi);
+                            if constexpr (kMasked) tc_st8(to + 16, low);
+                        };
+#pragma unroll 1
+                        for (int c = 0; c < 8; c += 2) {
+                            tc_wait_ld();
+                            tc_ld16(y, s_at + 16 * (c + 1));
+                            tc_wait_ld();       // both halves of P's 32 columns are read before they are written
+                            weigh(x, c);
+                            if (c < 6) tc_ld16(x, s_at + 16 * (c + 2));
+                            weigh(y, c + 1);
                         }
                         tc_wait_st();
                     };
@@ -509,19 +584,27 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
                 }
                 tc_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.p_full[gr]);
+                if (lane == 0) mbar_arrive(&bars.p_full[sb]);
             }
+            if (two) {
+                s_seen[0] += g.tiles;
+                s_seen[1] += g.tiles;
+            } else {
+                s_seen[0] += (g.tiles + 1) >> 1;
+                s_seen[1] += g.tiles >> 1;
+                pv_seen += g.tiles;
+            }
+            const float l = l2.x + l2.y, lr = lr2.x + lr2.y;
 
             // ---- the next unit's Q, then this one's output ------------------------
             const Segment cur = g;
             const long long next = cur.u_from + cur.v1;
-            const bool more = next < share.hi;
+            const bool more = next < share.hi();
             if (more) {
                 g = share.segment(next);
                 if (g.tiles > 0) load_q(g);
             }
-            const bool mine = MT == 2 ? cur.tiles > 0 : cur.tiles > k0;     // this group has an O
-            if (mine) {
+            if (mine > 0) {
                 wait(&bars.o_done[gr], o_seen++ & 1u);
                 tc_after();
             }
@@ -532,7 +615,7 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
             int c0 = blockIdx.x, parts = 1;
             if (!whole) share.sharers(cur, c0, parts);
             const int slot = 2 * static_cast<int>(blockIdx.x) + (c0 == static_cast<int>(blockIdx.x) ? 1 : 0);
-            const long long part_row = static_cast<long long>(slot) * Cfg::kRows + row;
+            const long long part_row = static_cast<long long>(slot) * kRows + row;
             // 32 columns of O, in the order of the decoded values, into the output
             // or into the unit's parts
             auto emit = [&](int c, const float (&v)[32], bool on, float f) {
@@ -557,83 +640,19 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
                     for (int e = 0; e < 8; ++e) __stcg(to + e, make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]));
                 }
             };
-            const bool any_here = (row & ~31) < cur.live_rows;
-            if constexpr (MT == 2) {
-#pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    float v[32] = {};
-                    if (mine && any_here) {
-                        tc_ld32(v, o_at + 32 * c);
-                        tc_wait_ld();
-                    }
-                    finish(c, v);
-                }
-                tc_before();
-                __syncwarp();
-                if (mine && lane == 0) mbar_arrive(&bars.o_free[gr]);
-            } else {
-                // group 1's half is added to group 0's, 64 columns at a time
-                const uint32_t jrow = join + r * 256;
-                float f0 = 1.0f, f1 = 0.0f;
-                if (gr == 1) {
-                    s_join[r][0] = m;
-                    s_join[r][1] = l;
-                    s_join[r][2] = lr;
-                }
 #pragma unroll 1
-                for (int half = 0; half < D / 64; ++half) {
-                    if (gr == 1) {
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            float v[32] = {};
-                            if (mine && any_here) {
-                                tc_ld32(v, o_at + 64 * half + 32 * c);
-                                tc_wait_ld();
-                            }
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                sts128(jrow + (((8 * c + e) ^ (r & 15)) << 4), __float_as_uint(v[4 * e]), __float_as_uint(v[4 * e + 1]),
-                                       __float_as_uint(v[4 * e + 2]), __float_as_uint(v[4 * e + 3]));
-                        }
-                    }
-                    asm volatile("bar.sync 3, 256;" ::: "memory");
-                    if (gr == 0) {
-                        if (half == 0) {
-                            const float m1 = s_join[r][0], mn = fmaxf(m, m1);
-                            f0 = exp2_fast(m - mn);
-                            f1 = exp2_fast(m1 - mn);
-                            m = mn;
-                            l = l * f0 + s_join[r][1] * f1;
-                            lr = lr * f0 + s_join[r][2] * f1;
-                        }
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            float v[32] = {};
-                            if (mine && any_here) {
-                                tc_ld32(v, o_at + 64 * half + 32 * c);
-                                tc_wait_ld();
-                            }
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                float4 y;
-                                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                                             : "=f"(y.x), "=f"(y.y), "=f"(y.z), "=f"(y.w)
-                                             : "r"(jrow + (((8 * c + e) ^ (r & 15)) << 4)));
-                                v[4 * e] = v[4 * e] * f0 + y.x * f1;
-                                v[4 * e + 1] = v[4 * e + 1] * f0 + y.y * f1;
-                                v[4 * e + 2] = v[4 * e + 2] * f0 + y.z * f1;
-                                v[4 * e + 3] = v[4 * e + 3] * f0 + y.w * f1;
-                            }
-                            finish(2 * half + c, v);
-                        }
-                    }
-                    asm volatile("bar.sync 3, 256;" ::: "memory");
+            for (int c = 0; c < D / 32; ++c) {
+                float v[32] = {};
+                if (mine > 0 && warp_live) {
+                    tc_ld32(v, o_at + 32 * c);
+                    tc_wait_ld();
                 }
-                tc_before();
-                __syncwarp();
-                if (mine && lane == 0) mbar_arrive(&bars.o_free[gr]);
+                finish(c, v);
             }
-            if (MT == 2 || gr == 0) {
+            tc_before();
+            __syncwarp();
+            if (mine > 0 && lane == 0) mbar_arrive(&bars.o_free[gr]);
+            {
                 if (whole) {
                     if (exists && A.lse) A.lse[at_row] = live && l != 0.0f ? (m + log2f(l)) * kLn2 : -CUDART_INF_F;
                 } else {
@@ -649,7 +668,7 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
                     group_sync(gr);
                     if (s_last[gr]) {
                         __threadfence();
-                        auto place = [&](int c) { return (2ll * (c0 + c) + (c == 0 ? 1 : 0)) * Cfg::kRows + row; };
+                        auto place = [&](int c) { return (2ll * (c0 + c) + (c == 0 ? 1 : 0)) * kRows + row; };
                         float mm = kNoMax, sum = 0.0f, rsum = 0.0f;
                         if (live) {
 #pragma unroll 4
@@ -696,15 +715,15 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
     if (warp == kMmaWarp) tc_dealloc(tmem, 512);
 }
 
-template <int D, int MT>
+template <int D>
 cudaError_t attend_tc(const CacheAttendArgs& A, cudaStream_t st) {
-    using Cfg = TcCfg<D, MT>;
+    using Cfg = TcCfg<D>;
     const int grid = min(attend_sms(), kMaxGrid / 2);
-    const AttendLayout y(2 * grid, Cfg::kRows, D);
+    const AttendLayout y(2 * grid, kRows, D);
     AttendPlan L;
     L.one2 = 0x3F803F80u;
     L.grid = grid;
-    L.row_tiles = (A.n * A.G + Cfg::kRows - 1) / Cfg::kRows;
+    L.row_tiles = (A.n * A.G + kRows - 1) / kRows;
     L.min_tiles = 2;
     const long long tiles = ((static_cast<long long>(A.tab.width) << A.pool.p_shift) + A.n) / kTok + 2;
     if (tiles * A.pool.heads * L.row_tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
@@ -715,25 +734,21 @@ cudaError_t attend_tc(const CacheAttendArgs& A, cudaStream_t st) {
     static std::atomic<unsigned long long> ready{0};
     const int dev = attend_device();
     if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
-        const cudaError_t e = cudaFuncSetAttribute(cache_attend_tc_kernel<D, MT>,
+        const cudaError_t e = cudaFuncSetAttribute(cache_attend_tc_kernel<D>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
         if (e != cudaSuccess) return e;
         if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
-    cache_attend_tc_kernel<D, MT><<<grid, kThreads, Cfg::kSmem, st>>>(A, L);
+    cache_attend_tc_kernel<D><<<grid, kThreads, Cfg::kSmem, st>>>(A, L);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t attend_tc_ws(int R, int D) {
-    return AttendLayout(2 * min(attend_sms(), kMaxGrid / 2), R <= 128 ? 128 : 256, D).bytes;
-}
+size_t attend_tc_ws(int D) { return AttendLayout(2 * min(attend_sms(), kMaxGrid / 2), kRows, D).bytes; }
 
 cudaError_t attend_tc_run(const CacheAttendArgs& A, cudaStream_t st) {
-    const bool one = A.n * A.G <= 128;
-    if (A.pool.D == 128) return one ? attend_tc<128, 1>(A, st) : attend_tc<128, 2>(A, st);
-    return one ? attend_tc<64, 1>(A, st) : attend_tc<64, 2>(A, st);
+    return A.pool.D == 128 ? attend_tc<128>(A, st) : attend_tc<64>(A, st);
 }
 
 }  // namespace spec
