@@ -70,18 +70,32 @@ __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(smem_u32(bar)) : "memory");
 }
+// A matrix in shared memory in 64-element (128-byte) chunks of 128 rows, 128-byte
+// swizzle: 8-row groups lie 1024 bytes apart, chunks 16384.  The low word of its
+// descriptor holds the address (in 16 bytes) and the chunks' distance; the high
+// word is constant.
+__device__ __forceinline__ uint32_t tc_desc(uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | ((16384u >> 4) << 16); }
+#define TC_DESC_HIGH "0x40004040"       /* 1024 bytes, version 1, 128-byte swizzle */
 // D = A B (+ D): both operands in shared memory, or A in tensor memory
-__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+template <bool kAdd>
+__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-        :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add) : "memory");
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 a, {%1, " TC_DESC_HIGH "};\n\tmov.b64 b, {%2, " TC_DESC_HIGH "};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}"
+        :: "r"(d), "r"(a), "r"(b), "r"(idesc), "n"(kAdd ? 1 : 0) : "memory");
 }
-__device__ __forceinline__ void tc_mma_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+__device__ __forceinline__ void tc_mma_ta(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-        :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(add) : "memory");
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 b, {%2, " TC_DESC_HIGH "};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}"
+        :: "r"(d), "r"(a), "r"(b), "r"(idesc), "r"(add) : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -121,12 +135,6 @@ __device__ __forceinline__ void tc_st16(uint32_t at, const uint32_t (&r)[16]) {
         : "memory");
 }
 
-// A matrix in shared memory in 64-element (128-byte) chunks of 128 rows, 128-byte
-// swizzle: 8-row groups lie 1024 bytes apart, chunks 16384.
-__device__ __forceinline__ uint64_t tc_desc(uint32_t addr) {
-    return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(16384 >> 4) << 16) |
-           (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
-}
 // kind::f16: fp32 accumulators, bf16 operands, M = 128, N columns; tb: B lies
 // with its N index contiguous
 constexpr uint32_t tc_idesc(int N, bool tb) {
@@ -335,7 +343,7 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
     } else if (warp >= kMmaWarp) {
         // ---- the tensor core's thread -----------------------------------------
         regs_down<kRegsIssue>();
-        if (warp == kMmaWarp && lane == 0) {
+        if (warp == kMmaWarp) {                 // (the whole warp keeps step, one thread issues)
             constexpr uint32_t kQk = tc_idesc(128, false), kPv = tc_idesc(D, true);
             uint32_t tiles_done = 0, segs = 0, p_seen[2] = {0, 0}, o_seen[2] = {0, 0};
             for (long long pos = share.lo(); pos < share.hi();) {
@@ -354,22 +362,29 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
                     const uint32_t n = tiles_done + (two ? i >> 1 : i), buf = n & 1;
                     if (!two || gr == 0) wait(&bars.k_full[buf], (n >> 1) & 1u);
                     tc_after();
-                    const uint32_t q = q_buf + (two ? gr : 0) * Cfg::kQBytes, kb = k_buf + buf * kTile;
-                    if (!s_dead) {
+                    const uint32_t q = __shfl_sync(0xffffffffu, tc_desc(q_buf + (two ? gr : 0) * Cfg::kQBytes), 0);
+                    const uint32_t kb = __shfl_sync(0xffffffffu, tc_desc(k_buf + buf * kTile), 0);
+                    const uint32_t to = __shfl_sync(0xffffffffu, tmem + kS(gr), 0);
+                    if (elect_one()) {
+                        if (!s_dead) {
+                            tc_mma<false>(to, q, kb, kQk);
 #pragma unroll
-                        for (int j = 0; j < D / 16; ++j) {
-                            const uint32_t at = (j >> 2) * kChunk + (j & 3) * 32;
-                            tc_mma(tmem + kS(gr), tc_desc(q + at), tc_desc(kb + at), kQk, j > 0);
+                            for (int j = 1; j < D / 16; ++j) {
+                                const uint32_t at = ((j >> 2) * kChunk + (j & 3) * 32) >> 4;
+                                tc_mma<true>(to, q + at, kb + at, kQk);
+                            }
                         }
+                        tc_commit(&bars.s_full[gr]);
+                        if (!two || gr == 1) tc_commit(&bars.k_empty[buf]);
+                        if (i == jobs - 1) tc_commit(&bars.q_empty);
                     }
-                    tc_commit(&bars.s_full[gr]);
-                    if (!two || gr == 1) tc_commit(&bars.k_empty[buf]);
-                    if (i == jobs - 1) tc_commit(&bars.q_empty);
+                    __syncwarp();
                 };
                 auto pv = [&](int i) {
                     const int sb = i & 1, gr = two ? sb : 0, k = two ? i >> 1 : i;
                     const uint32_t n = tiles_done + k, buf = n & 1;
                     const bool first = k == 0, last = k == g.tiles - 1;
+                    const bool lo = rq.partial(A, rq.real(g.v0 + k) * kTok);
                     wait(&bars.p_full[sb], p_seen[sb]++ & 1u);
                     if (gr == 0) wait(&bars.v_full[buf], (n >> 1) & 1u);
                     if (first) {                // O is written anew: the last unit's has been read
@@ -377,20 +392,24 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
                         ++o_seen[gr];
                     }
                     tc_after();
-                    const bool lo = rq.partial(A, rq.real(g.v0 + k) * kTok);
-                    const uint32_t vb = v_buf + buf * kTile;
-                    if (!s_dead) {
+                    const uint32_t vb = __shfl_sync(0xffffffffu, tc_desc(v_buf + buf * kTile), 0);
+                    const uint32_t p = __shfl_sync(0xffffffffu, tmem + kS(sb), 0);
+                    const uint32_t to = __shfl_sync(0xffffffffu, tmem + kO(gr), 0);
+                    if (elect_one()) {
+                        if (!s_dead) {
 #pragma unroll
-                        for (int j = 0; j < kTok / 16; ++j) {
-                            const uint32_t p = tmem + kS(sb) + 32 * (j >> 1) + 8 * (j & 1);
-                            const uint64_t vd = tc_desc(vb + j * 2048);
-                            tc_mma_ta(tmem + kO(gr), p, vd, kPv, !first || j > 0);
-                            if (lo) tc_mma_ta(tmem + kO(gr), p + 16, vd, kPv, 1);
+                            for (int j = 0; j < kTok / 16; ++j)
+                                tc_mma_ta(to, p + 32 * (j >> 1) + 8 * (j & 1), vb + j * 128, kPv, j > 0 ? 1u : !first);
+                            if (lo)
+#pragma unroll
+                                for (int j = 0; j < kTok / 16; ++j)
+                                    tc_mma_ta(to, p + 32 * (j >> 1) + 8 * (j & 1) + 16, vb + j * 128, kPv, 1);
                         }
+                        if (!two) tc_commit(&bars.pv_done);
+                        if (!two || gr == 1) tc_commit(&bars.v_empty[buf]);
+                        if (last) tc_commit(&bars.o_done[gr]);
                     }
-                    if (!two) tc_commit(&bars.pv_done);
-                    if (!two || gr == 1) tc_commit(&bars.v_empty[buf]);
-                    if (last) tc_commit(&bars.o_done[gr]);
+                    __syncwarp();
                 };
                 qk(0);
                 if (jobs > 1) qk(1);
@@ -682,26 +701,42 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
                             }
                         }
                         const bool on = live && sum != 0.0f;
-                        if (exists) {
-#pragma unroll 1
-                            for (int q = 0; q < D / 32; ++q) {
-                                float v[32] = {};
-                                if (live)
-                                    for (int c = 0; c < parts; ++c) {
-                                        const float f = exp2_fast(__ldcg(L.ml + place(c) * 4) - mm);
-                                        const float4* from = reinterpret_cast<const float4*>(L.part + place(c) * D + 32 * q);
-#pragma unroll
-                                        for (int e = 0; e < 8; ++e) {
-                                            const float4 y = __ldcg(from + e);
-                                            v[4 * e] += f * y.x;
-                                            v[4 * e + 1] += f * y.y;
-                                            v[4 * e + 2] += f * y.z;
-                                            v[4 * e + 3] += f * y.w;
-                                        }
+                        if (exists && A.lse) A.lse[at_row] = on ? (mm + log2f(sum)) * kLn2 : -CUDART_INF_F;
+                        // the values a row a warp: a lane has D/32 columns, 4 (2) of a
+                        // group of 8 in the order 0 4 1 5 2 6 3 7
+                        const float scale = on ? 16.0f / rsum : 0.0f;
+                        const unsigned there = __ballot_sync(0xffffffffu, exists);
+#pragma unroll 2
+                        for (int q = 0; q < 32; ++q) {
+                            if (!(there >> q & 1u)) continue;
+                            const float top = __shfl_sync(0xffffffffu, mm, q), f_out = __shfl_sync(0xffffffffu, scale, q);
+                            const long long at = __shfl_sync(0xffffffffu, at_row, q);
+                            const int row_q = (row & ~31) + q;
+                            float v[D / 32] = {};
+                            if (f_out != 0.0f)
+#pragma unroll 4
+                                for (int c = 0; c < parts; ++c) {
+                                    const long long from = (2ll * (c0 + c) + (c == 0 ? 1 : 0)) * kRows + row_q;
+                                    const float f = exp2_fast(__ldcg(L.ml + from * 4) - top);
+                                    const float* x = L.part + from * D + lane * (D / 32);
+                                    if constexpr (D == 128) {
+                                        const float4 y = __ldcg(reinterpret_cast<const float4*>(x));
+                                        v[0] += f * y.x; v[1] += f * y.y; v[2] += f * y.z; v[3] += f * y.w;
+                                    } else {
+                                        const float2 y = __ldcg(reinterpret_cast<const float2*>(x));
+                                        v[0] += f * y.x; v[1] += f * y.y;
                                     }
-                                emit(q, v, on, on ? 16.0f / rsum : 0.0f);
+                                }
+                            uint16_t* to = A.out + at * D;
+                            if constexpr (D == 128) {
+                                to += 8 * (lane >> 1) + 2 * (lane & 1);
+                                *reinterpret_cast<uint32_t*>(to) = pack_bf16(v[0] * f_out, v[2] * f_out);
+                                *reinterpret_cast<uint32_t*>(to + 4) = pack_bf16(v[1] * f_out, v[3] * f_out);
+                            } else {
+                                to += 8 * (lane >> 2) + (lane & 3);
+                                to[0] = __bfloat16_as_ushort(__float2bfloat16_rn(v[0] * f_out));
+                                to[4] = __bfloat16_as_ushort(__float2bfloat16_rn(v[1] * f_out));
                             }
-                            if (A.lse) A.lse[at_row] = on ? (mm + log2f(sum)) * kLn2 : -CUDART_INF_F;
                         }
                     }
                 }
