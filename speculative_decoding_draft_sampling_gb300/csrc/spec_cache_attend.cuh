@@ -82,6 +82,12 @@ struct Req {
     __device__ __forceinline__ bool needs(const CacheAttendArgs& A, int t0, int t1) const {
         return t0 < len && (A.window == 0 || t0 < A.sinks || t1 > low);
     }
+    // Visited tiles [from, to) are such that every row sees every key (there may be
+    // others: a range that costs nothing to look up).
+    __device__ __forceinline__ void plain(const CacheAttendArgs& A, int& from, int& to) const {
+        from = A.window > 0 ? sink_tiles + max(0, (low + A.n + kTile - 1) / kTile - first) : 0;
+        to = sink_tiles + ctx / kTile - first;
+    }
     // whether some row may not see some key of the tile at t0
     __device__ __forceinline__ bool partial(const CacheAttendArgs& A, int t0) const {
         return t0 + kTile > ctx || (A.window > 0 && t0 + kTile > A.sinks && t0 < low + A.n);

@@ -355,6 +355,10 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
                 // groups, else in turn
                 const bool two = g.live_rows > 128;
                 const int jobs = two ? 2 * g.tiles : g.tiles;
+                int plain0, plain1;
+                rq.plain(A, plain0, plain1);
+                plain0 -= g.v0;
+                plain1 -= g.v0;
                 wait(&bars.q_full, segs & 1u);
                 ++segs;
                 auto qk = [&](int i) {
@@ -384,7 +388,7 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
                     const int sb = i & 1, gr = two ? sb : 0, k = two ? i >> 1 : i;
                     const uint32_t n = tiles_done + k, buf = n & 1;
                     const bool first = k == 0, last = k == g.tiles - 1;
-                    const bool lo = rq.partial(A, rq.real(g.v0 + k) * kTok);
+                    const bool lo = k < plain0 || k >= plain1;
                     wait(&bars.p_full[sb], p_seen[sb]++ & 1u);
                     if (gr == 0) wait(&bars.v_full[buf], (n >> 1) & 1u);
                     if (first) {                // O is written anew: the last unit's has been read
@@ -441,7 +445,7 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
             const uint16_t* q = A.q + g.b * A.q_bs + i * A.q_rs + (static_cast<long long>(g.h) * A.G + gq) * A.q_hs;
             const uint32_t to = q_buf + gr * Cfg::kQBytes;
             if (on) {
-#pragma unroll 8
+#pragma unroll
                 for (int j = 0; j < D / 8; ++j) {
                     uint4 x;
                     if (A.aligned) {
@@ -471,37 +475,55 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
             float m = kNoMax;
             float2 l2 = make_float2(0.0f, 0.0f), lr2 = l2;      // two partial sums each
             const int mine = two || gr == 0 ? g.tiles : 0;      // this group's tiles
-            // which of a tile's pages are missing: a lane a page, looked up a tile
-            // ahead and judged when its turn comes
-            int page = 0;
-            auto look_up = [&](int k) {
-                page = 0;
-                if (k >= mine || lane >= kTok >> p_shift) return;
-                const int at = rq.real(g.v0 + k) * kTok + (lane << p_shift);
-                if (rq.needs(A, at, at + P))
-                    page = (at >> p_shift) < A.tab.width
-                               ? static_cast<int>(ldg_now_u32(A.tab.table + g.b * A.tab.stride + (at >> p_shift)))
-                               : -1;
+            // Whether pages are missing is asked for all of the unit's tiles at once; a
+            // unit where some are looks them up again tile by tile.
+            auto page_at = [&](int at) {
+                if (!rq.needs(A, at, at + P)) return 0;
+                return (at >> p_shift) < A.tab.width
+                           ? static_cast<int>(ldg_now_u32(A.tab.table + g.b * A.tab.stride + (at >> p_shift)))
+                           : -1;
             };
-            look_up(0);
+            bool missing = false;
+            {
+                const int per = kTok >> p_shift, pages = mine << (7 - p_shift);
+                for (int x0 = 0; x0 < pages; x0 += 128) {
+                    int page[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int x = x0 + 32 * q + lane;
+                        page[q] = x < pages ? page_at(rq.real(g.v0 + (x >> (7 - p_shift))) * kTok + ((x & (per - 1)) << p_shift)) : 0;
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        missing |= static_cast<unsigned>(page[q]) >= static_cast<unsigned>(A.pool.num_pages);
+                }
+                missing = __any_sync(0xffffffffu, missing);
+            }
+            int plain0, plain1;
+            rq.plain(A, plain0, plain1);
+            plain0 -= g.v0;
+            plain1 -= g.v0;
             for (int k = 0; k < mine; ++k) {
                 const int sb = two ? gr : k & 1;
                 const uint32_t s_at = tmem + kS(sb) + lanes;
-                const int t0 = rq.real(g.v0 + k) * kTok;
-                const uint32_t gone =
-                    __ballot_sync(0xffffffffu, static_cast<unsigned>(page) >= static_cast<unsigned>(A.pool.num_pages));
-                look_up(k + 1);
-                const bool lo = rq.partial(A, t0);
+                const bool lo = k < plain0 || k >= plain1;
                 unsigned long long seen0 = ~0ull, seen1 = ~0ull;
-                if (warp_live && (lo || gone)) {
-                    seen0 = live ? seen64(A, rq, g.b, qi, t0) : 0;
-                    seen1 = live ? seen64(A, rq, g.b, qi, t0 + 64) : 0;
+                if (lo || missing) {
+                    const int t0 = rq.real(g.v0 + k) * kTok;
+                    if (live) {
+                        seen0 = seen64(A, rq, g.b, qi, t0);
+                        seen1 = seen64(A, rq, g.b, qi, t0 + 64);
+                    }
+                    if (missing) {
+                        const int page = lane < kTok >> p_shift ? page_at(t0 + (lane << p_shift)) : 0;
 #pragma unroll 1
-                    for (uint32_t x = gone; x; x &= x - 1) {
-                        const int a = (__ffs(x) - 1) << p_shift;
-                        const unsigned long long off = range64(a & 63, (a & 63) + P, 0);
-                        if (a < 64) seen0 &= ~off;
-                        else seen1 &= ~off;
+                        for (uint32_t x = __ballot_sync(0xffffffffu, static_cast<unsigned>(page) >= static_cast<unsigned>(A.pool.num_pages));
+                             x; x &= x - 1) {
+                            const int a = (__ffs(x) - 1) << p_shift;
+                            const unsigned long long off = range64(a & 63, (a & 63) + P, 0);
+                            if (a < 64) seen0 &= ~off;
+                            else seen1 &= ~off;
+                        }
                     }
                 }
                 wait(&bars.s_full[sb], ((sb ? s_seen[1] : s_seen[0]) + (two ? k : k >> 1)) & 1u);
@@ -598,7 +620,7 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
                         }
                         tc_wait_st();
                     };
-                    if (lo || gone) tile(std::true_type{});
+                    if (lo || missing) tile(std::true_type{});
                     else tile(std::false_type{});
                 }
                 tc_before();
@@ -702,40 +724,52 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
                         }
                         const bool on = live && sum != 0.0f;
                         if (exists && A.lse) A.lse[at_row] = on ? (mm + log2f(sum)) * kLn2 : -CUDART_INF_F;
-                        // the values a row a warp: a lane has D/32 columns, 4 (2) of a
-                        // group of 8 in the order 0 4 1 5 2 6 3 7
+                        // The values, a row a warp, 16 rows in flight: a lane has D/32
+                        // columns, 4 (2) of a group of 8 in the order 0 4 1 5 2 6 3 7.
                         const float scale = on ? 16.0f / rsum : 0.0f;
                         const unsigned there = __ballot_sync(0xffffffffu, exists);
-#pragma unroll 2
-                        for (int q = 0; q < 32; ++q) {
-                            if (!(there >> q & 1u)) continue;
-                            const float top = __shfl_sync(0xffffffffu, mm, q), f_out = __shfl_sync(0xffffffffu, scale, q);
-                            const long long at = __shfl_sync(0xffffffffu, at_row, q);
-                            const int row_q = (row & ~31) + q;
-                            float v[D / 32] = {};
-                            if (f_out != 0.0f)
-#pragma unroll 4
-                                for (int c = 0; c < parts; ++c) {
-                                    const long long from = (2ll * (c0 + c) + (c == 0 ? 1 : 0)) * kRows + row_q;
-                                    const float f = exp2_fast(__ldcg(L.ml + from * 4) - top);
-                                    const float* x = L.part + from * D + lane * (D / 32);
-                                    if constexpr (D == 128) {
-                                        const float4 y = __ldcg(reinterpret_cast<const float4*>(x));
-                                        v[0] += f * y.x; v[1] += f * y.y; v[2] += f * y.z; v[3] += f * y.w;
-                                    } else {
-                                        const float2 y = __ldcg(reinterpret_cast<const float2*>(x));
-                                        v[0] += f * y.x; v[1] += f * y.y;
-                                    }
-                                }
+                        constexpr int kRow = 16;
+                        auto emit_row = [&](long long at, const float (&v)[D / 32], float f) {
                             uint16_t* to = A.out + at * D;
+                            float y[D / 32];
+#pragma unroll
+                            for (int e = 0; e < D / 32; ++e) y[e] = f == 0.0f ? 0.0f : v[e] * f;
                             if constexpr (D == 128) {
                                 to += 8 * (lane >> 1) + 2 * (lane & 1);
-                                *reinterpret_cast<uint32_t*>(to) = pack_bf16(v[0] * f_out, v[2] * f_out);
-                                *reinterpret_cast<uint32_t*>(to + 4) = pack_bf16(v[1] * f_out, v[3] * f_out);
+                                *reinterpret_cast<uint32_t*>(to) = pack_bf16(y[0], y[2]);
+                                *reinterpret_cast<uint32_t*>(to + 4) = pack_bf16(y[1], y[3]);
                             } else {
                                 to += 8 * (lane >> 2) + (lane & 3);
-                                to[0] = __bfloat16_as_ushort(__float2bfloat16_rn(v[0] * f_out));
-                                to[4] = __bfloat16_as_ushort(__float2bfloat16_rn(v[1] * f_out));
+                                to[0] = __bfloat16_as_ushort(__float2bfloat16_rn(y[0]));
+                                to[4] = __bfloat16_as_ushort(__float2bfloat16_rn(y[1]));
+                            }
+                        };
+#pragma unroll 1
+                        for (int q0 = 0; q0 < 32; q0 += kRow) {
+                            if (!(there >> q0)) break;
+                            float v[kRow][D / 32] = {};
+                            for (int c = 0; c < parts; ++c) {
+                                const float f_own = live ? exp2_fast(__ldcg(L.ml + place(c) * 4) - mm) : 0.0f;
+                                const long long from = (2ll * (c0 + c) + (c == 0 ? 1 : 0)) * kRows + (row & ~31) + q0;
+                                const float* x = L.part + from * D + lane * (D / 32);
+                                // (rows that are not there: whatever lies in the parts, not used)
+#pragma unroll
+                                for (int q = 0; q < kRow; ++q) {
+                                    const float f = __shfl_sync(0xffffffffu, f_own, q0 + q);
+                                    if constexpr (D == 128) {
+                                        const float4 y = __ldcg(reinterpret_cast<const float4*>(x + q * D));
+                                        v[q][0] += f * y.x; v[q][1] += f * y.y; v[q][2] += f * y.z; v[q][3] += f * y.w;
+                                    } else {
+                                        const float2 y = __ldcg(reinterpret_cast<const float2*>(x + q * D));
+                                        v[q][0] += f * y.x; v[q][1] += f * y.y;
+                                    }
+                                }
+                            }
+#pragma unroll
+                            for (int q = 0; q < kRow; ++q) {
+                                const float f = __shfl_sync(0xffffffffu, scale, q0 + q);
+                                const long long at = __shfl_sync(0xffffffffu, at_row, q0 + q);
+                                if (there >> (q0 + q) & 1u) emit_row(at, v[q], f);
                             }
                         }
                     }
