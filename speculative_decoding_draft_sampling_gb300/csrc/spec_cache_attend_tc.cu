@@ -37,9 +37,9 @@ constexpr int kWarps = 20;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMmaWarp = 16;
 // Registers a thread: 96 at launch (640 threads), then moved from the decoders and
-// the issuing group to the softmax: 256 * 72 + 128 * 72 + 256 * 128 = 60416 of the
+// the issuing group to the softmax: 256 * 64 + 128 * 72 + 256 * 136 = 60416 of the
 // 61440 that the block was launched with.
-constexpr int kRegsDecode = 72, kRegsIssue = 72, kRegsSoftmax = 128;
+constexpr int kRegsDecode = 64, kRegsIssue = 72, kRegsSoftmax = 136;
 static_assert(256 * kRegsDecode + 128 * kRegsIssue + 256 * kRegsSoftmax <= 96 * kThreads, "register shares");
 
 constexpr int kRows = 256;                      // rows a unit
@@ -361,66 +361,67 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
                 plain1 -= g.v0;
                 wait(&bars.q_full, segs & 1u);
                 ++segs;
-                auto qk = [&](int i) {
-                    const int gr = i & 1;
-                    const uint32_t n = tiles_done + (two ? i >> 1 : i), buf = n & 1;
-                    if (!two || gr == 0) wait(&bars.k_full[buf], (n >> 1) & 1u);
-                    tc_after();
-                    const uint32_t q = __shfl_sync(0xffffffffu, tc_desc(q_buf + (two ? gr : 0) * Cfg::kQBytes), 0);
-                    const uint32_t kb = __shfl_sync(0xffffffffu, tc_desc(k_buf + buf * kTile), 0);
-                    const uint32_t to = __shfl_sync(0xffffffffu, tmem + kS(gr), 0);
-                    if (elect_one()) {
-                        if (!s_dead) {
-                            tc_mma<false>(to, q, kb, kQk);
-#pragma unroll
-                            for (int j = 1; j < D / 16; ++j) {
-                                const uint32_t at = ((j >> 2) * kChunk + (j & 3) * 32) >> 4;
-                                tc_mma<true>(to, q + at, kb + at, kQk);
-                            }
+                // The products S = Q K^T of job i, if there is one, and of the job two
+                // before it O += P V.  What they need is waited for with P last, and S
+                // is committed first: the softmax waits for nothing else.
+                auto step = [&](int i) {
+                    const int pj = i - 2;
+                    const int sb = i & 1;
+                    const bool s_on = i < jobs, p_on = pj >= 0;
+                    const int k_s = two ? i >> 1 : i, k_p = two ? pj >> 1 : pj, gr = two ? sb : 0;
+                    const uint32_t n_s = tiles_done + k_s, n_p = tiles_done + k_p;
+                    const bool first = k_p == 0, last = k_p == g.tiles - 1;
+                    const bool lo = k_p < plain0 || k_p >= plain1;
+                    const uint32_t q = __shfl_sync(0xffffffffu, tc_desc(q_buf + gr * Cfg::kQBytes), 0);
+                    const uint32_t kb = __shfl_sync(0xffffffffu, tc_desc(k_buf + (n_s & 1) * kTile), 0);
+                    const uint32_t vb = __shfl_sync(0xffffffffu, tc_desc(v_buf + (n_p & 1) * kTile), 0);
+                    const uint32_t s_to = __shfl_sync(0xffffffffu, tmem + kS(sb), 0);
+                    const uint32_t o_to = __shfl_sync(0xffffffffu, tmem + kO(gr), 0);
+                    if (s_on && gr == 0) wait(&bars.k_full[n_s & 1], (n_s >> 1) & 1u);
+                    if (p_on) {
+                        if (gr == 0) wait(&bars.v_full[n_p & 1], (n_p >> 1) & 1u);
+                        if (first) {            // O is written anew: the last unit's has been read
+                            wait(&bars.o_free[gr], (o_seen[gr] & 1u) ^ 1u);
+                            ++o_seen[gr];
                         }
-                        tc_commit(&bars.s_full[gr]);
-                        if (!two || gr == 1) tc_commit(&bars.k_empty[buf]);
-                        if (i == jobs - 1) tc_commit(&bars.q_empty);
-                    }
-                    __syncwarp();
-                };
-                auto pv = [&](int i) {
-                    const int sb = i & 1, gr = two ? sb : 0, k = two ? i >> 1 : i;
-                    const uint32_t n = tiles_done + k, buf = n & 1;
-                    const bool first = k == 0, last = k == g.tiles - 1;
-                    const bool lo = k < plain0 || k >= plain1;
-                    wait(&bars.p_full[sb], p_seen[sb]++ & 1u);
-                    if (gr == 0) wait(&bars.v_full[buf], (n >> 1) & 1u);
-                    if (first) {                // O is written anew: the last unit's has been read
-                        wait(&bars.o_free[gr], (o_seen[gr] & 1u) ^ 1u);
-                        ++o_seen[gr];
+                        wait(&bars.p_full[sb], p_seen[sb]++ & 1u);
                     }
                     tc_after();
-                    const uint32_t vb = __shfl_sync(0xffffffffu, tc_desc(v_buf + buf * kTile), 0);
-                    const uint32_t p = __shfl_sync(0xffffffffu, tmem + kS(sb), 0);
-                    const uint32_t to = __shfl_sync(0xffffffffu, tmem + kO(gr), 0);
                     if (elect_one()) {
-                        if (!s_dead) {
+                        if (p_on && !s_dead) {
 #pragma unroll
                             for (int j = 0; j < kTok / 16; ++j)
-                                tc_mma_ta(to, p + 32 * (j >> 1) + 8 * (j & 1), vb + j * 128, kPv, j > 0 ? 1u : !first);
+                                tc_mma_ta(o_to, s_to + 16 * j, vb + j * 128, kPv, j > 0 ? 1u : !first);
                             if (lo)
 #pragma unroll
                                 for (int j = 0; j < kTok / 16; ++j)
-                                    tc_mma_ta(to, p + 32 * (j >> 1) + 8 * (j & 1) + 16, vb + j * 128, kPv, 1);
+                                    tc_mma_ta(o_to, s_to + 16 * j + 8, vb + j * 128, kPv, 1);
                         }
-                        if (!two) tc_commit(&bars.pv_done);
-                        if (!two || gr == 1) tc_commit(&bars.v_empty[buf]);
-                        if (last) tc_commit(&bars.o_done[gr]);
+                        // (before S: whoever sees S of job i sees this of job i - 2)
+                        if (p_on && !two) tc_commit(&bars.pv_done);
+                        if (s_on) {
+                            if (!s_dead) {
+                                tc_mma<false>(s_to, q, kb, kQk);
+#pragma unroll
+                                for (int j = 1; j < D / 16; ++j) {
+                                    const uint32_t at = ((j >> 2) * kChunk + (j & 3) * 32) >> 4;
+                                    tc_mma<true>(s_to, q + at, kb + at, kQk);
+                                }
+                            }
+                            tc_commit(&bars.s_full[sb]);
+                        }
+                        if (p_on) {
+                            if (last) tc_commit(&bars.o_done[gr]);
+                            if (!two || gr == 1) tc_commit(&bars.v_empty[n_p & 1]);
+                        }
+                        if (s_on) {
+                            if (!two || gr == 1) tc_commit(&bars.k_empty[n_s & 1]);
+                            if (i == jobs - 1) tc_commit(&bars.q_empty);
+                        }
                     }
                     __syncwarp();
                 };
-                qk(0);
-                if (jobs > 1) qk(1);
-                for (int i = 0; i < jobs; ++i) {
-                    pv(i);
-                    if (i + 2 < jobs) qk(i + 2);
-                }
+                for (int i = 0; i < jobs + 2; ++i) step(i);
                 tiles_done += g.tiles;
             }
         }
@@ -604,17 +605,17 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
                                     lr2 = add2(lr2, h);
                                 }
                             }
-                            // P's 32 columns of S: 16 of weights, 16 of second terms
-                            const uint32_t to = s_at + 32 * (c >> 1) + 8 * (c & 1);
-                            tc_st8(to, hi);
-                            if constexpr (kMasked) tc_st8(to + 16, low);
+                            // P lies where its scores were: 8 columns of weights, 8 of
+                            // second terms
+                            tc_st8(s_at + 16 * c, hi);
+                            if constexpr (kMasked) tc_st8(s_at + 16 * c + 8, low);
                         };
 #pragma unroll 1
                         for (int c = 0; c < 8; c += 2) {
                             tc_wait_ld();
                             tc_ld16(y, s_at + 16 * (c + 1));
-                            tc_wait_ld();       // both halves of P's 32 columns are read before they are written
                             weigh(x, c);
+                            tc_wait_ld();
                             if (c < 6) tc_ld16(x, s_at + 16 * (c + 2));
                             weigh(y, c + 1);
                         }
