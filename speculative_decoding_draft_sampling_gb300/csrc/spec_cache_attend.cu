@@ -662,7 +662,7 @@ cudaError_t attend(const CacheAttendArgs& A, cudaStream_t st) {
     L.one2 = 0x3F803F80u;
     L.grid = grid;
     L.row_tiles = (A.n * A.G + Cfg::kRows - 1) / Cfg::kRows;
-    L.min_tiles = 3;
+    L.min_tiles = 1;
     // a request's tiles are counted in 32 bits
     const long long tiles = ((static_cast<long long>(A.tab.width) << A.pool.p_shift) + A.n) / kTile + 2;
     if (tiles * A.pool.heads * L.row_tiles > 0x7fffffffLL) return cudaErrorInvalidValue;

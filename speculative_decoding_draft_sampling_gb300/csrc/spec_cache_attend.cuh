@@ -165,23 +165,33 @@ struct Share {
             given = request_len(A, i);
             return static_cast<long long>(H) * Req<kTile>(A, given).head_work(A, L.row_tiles, rows_a_block);
         };
-        // the requests a chunk of threads at a time; one chunk is the usual case
-        long long first_work = 0, total = 0;            // (total: as the member, while it is counted)
-        for (int b0 = 0; b0 < A.B; b0 += kThreads) {
-            const long long v = work_of(b0 + tid);
-            if (b0 == 0) {
-                first_work = v;
-                scratch.len[tid] = given;
+        // Sums of all requests' tiles, a chunk of threads at a time; the chunk of the
+        // first requests, the only one in the usual case, is scanned as it is summed.
+        auto scan = [&](long long v, long long& before) {   // tiles before this thread's, and of the chunk
+            long long inc = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long t = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += t;
             }
-            total += v;
-        }
+            if (lane == 31) scratch.sum[warp] = inc;
+            __syncthreads();
+            long long all = 0;
+            before = inc - v;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-        if (lane == 0) scratch.sum[warp] = total;
-        __syncthreads();
-        total = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) total += scratch.sum[w];
+            for (int w = 0; w < kWarps; ++w) {
+                if (w < warp) before += scratch.sum[w];
+                all += scratch.sum[w];
+            }
+            __syncthreads();
+            return all;
+        };
+        const long long first_work = work_of(tid);
+        scratch.len[tid] = given;
+        long long first_before, unused;
+        const long long first_all = scan(first_work, first_before);
+        long long total = first_all;                        // (as the member, while it is counted)
+        for (int b0 = kThreads; b0 < A.B; b0 += kThreads) total += scan(work_of(b0 + tid), unused);
         const long long units = static_cast<long long>(A.B) * H * L.row_tiles;
         long long want = quotient(total, L.min_tiles);
         if (want > units * 64) want = units * 64;           // what joins a unit must stay small beside it
@@ -196,41 +206,31 @@ struct Share {
             active_ = active;
             lo_ = lo;
             hi_ = hi;
-        } else if (tid == 0) {
-            scratch.total = total;
-            scratch.active = active;
-            scratch.lo = lo;
-            scratch.hi = hi;
+        } else {
+            if (tid == 0) {
+                scratch.total = total;
+                scratch.active = active;
+                scratch.lo = lo;
+                scratch.hi = hi;
+            }
+            __syncthreads();
         }
-        __syncthreads();
         if (cta >= active) return;
         // the request that holds tile lo, and where its tiles start
-        long long before = 0;
-        for (int b0 = 0; b0 < A.B; b0 += kThreads) {
-            const long long v = b0 == 0 ? first_work : work_of(b0 + tid);
-            long long inc = v;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long t = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += t;
-            }
-            if (lane == 31) scratch.sum[warp] = inc;
-            __syncthreads();
-            long long base = before, all = 0;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                if (w < warp) base += scratch.sum[w];
-                all += scratch.sum[w];
-            }
-            const long long from = base + inc - v;
+        long long base = 0, v = first_work, before = first_before, all = first_all;
+        for (int b0 = 0;;) {
+            const long long from = base + before;
             if (v > 0 && from <= lo && lo < from + v) {
                 scratch.found[0] = b0 + tid;
                 scratch.found[1] = from;
             }
-            __syncthreads();
-            before += all;
-            if (lo < before) break;
+            base += all;
+            b0 += kThreads;
+            if (lo < base || b0 >= A.B) break;
+            v = work_of(b0 + tid);
+            all = scan(v, before);
         }
+        __syncthreads();
         b = static_cast<int>(scratch.found[0]);
         b_from = scratch.found[1];
         rq = req_at(b);

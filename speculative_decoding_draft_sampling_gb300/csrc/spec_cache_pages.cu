@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kPageThreads) cache_fork_kernel(const CachePag
 // codes in 16-byte pieces and scales a row at a time, a piece of each of kBlocks
 // blocks in flight a thread.  It may be launched while the fork's decisions are
 // still being made.
-constexpr int kBlocks = 4;
+constexpr int kBlocks = 2;
 
 template <int D>
 __global__ void __launch_bounds__(kCopyThreads) cache_copy_kernel(const CachePagesArgs A) {
