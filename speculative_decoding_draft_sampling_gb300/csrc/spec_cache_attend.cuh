@@ -17,6 +17,14 @@
 
 namespace spec {
 
+// Failure-path test builds (-DSPEC_TEST_HOOKS): when set, CTA 0 leaves out its first
+// copy (spec_cache_attend.cu) or the commit of its first scores
+// (spec_cache_attend_tc.cu), so that every wait that depends on it runs into its
+// limit and the kernel must leave with the workspace error set.
+#ifdef SPEC_TEST_HOOKS
+static __device__ int g_test_drop;
+#endif
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNoMax = -3.0e38f;              // the maximum before any key

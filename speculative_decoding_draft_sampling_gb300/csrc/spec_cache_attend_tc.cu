@@ -408,6 +408,9 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
                                     tc_mma<true>(s_to, q + at, kb + at, kQk);
                                 }
                             }
+#ifdef SPEC_TEST_HOOKS
+                            if (!(g_test_drop && blockIdx.x == 0 && i == 0))
+#endif
                             tc_commit(&bars.s_full[sb]);
                         }
                         if (p_on) {
@@ -611,14 +614,12 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
                             if constexpr (kMasked) tc_st8(s_at + 16 * c + 8, low);
                         };
 #pragma unroll 1
-                        for (int c = 0; c < 8; c += 2) {
+                        for (int c = 0; c < 8; ++c) {
                             tc_wait_ld();
-                            tc_ld16(y, s_at + 16 * (c + 1));
                             weigh(x, c);
-                            tc_wait_ld();
-                            if (c < 6) tc_ld16(x, s_at + 16 * (c + 2));
-                            weigh(y, c + 1);
+                            tc_ld16(x, s_at + 16 * ((c + 1) & 7));
                         }
+                        tc_wait_ld();
                         tc_wait_st();
                     };
                     if (lo || missing) tile(std::true_type{});
@@ -814,6 +815,10 @@ cudaError_t attend_tc(const CacheAttendArgs& A, cudaStream_t st) {
 }
 
 }  // namespace
+
+#ifdef SPEC_TEST_HOOKS
+extern "C" int spec_test_drop_commit(int on) { return static_cast<int>(cudaMemcpyToSymbol(g_test_drop, &on, sizeof(int))); }
+#endif
 
 size_t attend_tc_ws(int D) { return AttendLayout(2 * min(attend_sms(), kMaxGrid / 2), kRows, D).bytes; }
 
