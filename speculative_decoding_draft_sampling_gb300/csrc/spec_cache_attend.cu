@@ -161,12 +161,13 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
     const float cs = A.scale * kLog2e * 16.0f;
     const uint32_t one2 = L.one2;
 
-    // Copies, by warp 0: a lane per page block of the coming tiles.
+    // Copies: the warps take the tiles in turn, a lane per page block of the tiles that
+    // a warp will copy.
     int entry = -2;
     auto issue = [&](const Segment& g, int k, int s) {
-        const int in = k & ((32 >> ppt_shift) - 1);         // of the tiles whose page ids the lanes hold
+        const int in = (k >> 2) & ((32 >> ppt_shift) - 1);  // of the tiles whose page ids the lanes hold
         if (in == 0) {
-            const int v = g.v0 + k + (lane >> ppt_shift);
+            const int v = g.v0 + k + kAtWarps * (lane >> ppt_shift);
             entry = -2;
             if (v < g.v1) {
                 const int t = share.rq.real(v) * kTile + ((lane & (ppt - 1)) << p_shift);
@@ -203,10 +204,10 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
     // The start of a segment, as far as it can run beside the end of the one
     // before it: first copies, and Q's rows into the buffer of P^T.
     auto begin = [&](const Segment& g) {
-        if (warp == 0 && !s_dead)
+        if (!s_dead)
 #pragma unroll
             for (int s = 0; s < kS; ++s)
-                if (s < g.tiles) issue(g, s, s);
+                if (s < g.tiles && warp == (s & 3)) issue(g, s, s);
         if (A.aligned && g.tiles > 0) {
             for (int x = tid; x < kRows * (D / 8); x += kAtThreads) {
                 const int row = x / (D / 8), c = x % (D / 8), rho = g.row0 + row;
@@ -426,7 +427,7 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
                     __syncthreads();
                 }
                 // every warp is past the tile before this one: its stage is free
-                if (warp == 0 && k > 0 && k - 1 + kS < tiles && !s_dead) issue(g, k - 1 + kS, refill);
+                if (warp == ((k - 1 + kS) & 3) && k > 0 && k - 1 + kS < tiles && !s_dead) issue(g, k - 1 + kS, refill);
                 const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {

@@ -11,9 +11,9 @@
 //
 // One CTA an SM, in five warp groups (the fifth for one thread) that never wait
 // for each other all at once:
-//   warps 8-11   read the codes of a tile's 128 keys, a token a thread, two
-//                tiles ahead in registers, and write them as bf16 into shared
-//                memory (128-byte swizzle); warps 12-15 the same for the values;
+//   warps 8-11   read the codes of a tile's 128 keys, a token a thread, while the
+//                tile before waits, and write them as bf16 into shared memory
+//                (128-byte swizzle); warps 12-15 the same for the values;
 //   warp 16      one thread issues the tensor work: S_g = Q K^T (both in shared
 //                memory) and O_g += P_g V with P_g in tensor memory where S_g was;
 //   warps 0-3, 4-7  two softmax groups, g = 0 and 1, with 128 of a unit's 256 rows
@@ -37,9 +37,9 @@ constexpr int kWarps = 20;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMmaWarp = 16;
 // Registers a thread: 96 at launch (640 threads), then moved from the decoders and
-// the issuing group to the softmax: 256 * 64 + 128 * 72 + 256 * 136 = 60416 of the
+// the issuing group to the softmax: 256 * 56 + 128 * 72 + 256 * 144 = 60416 of the
 // 61440 that the block was launched with.
-constexpr int kRegsDecode = 64, kRegsIssue = 72, kRegsSoftmax = 136;
+constexpr int kRegsDecode = 56, kRegsIssue = 72, kRegsSoftmax = 144;
 static_assert(256 * kRegsDecode + 128 * kRegsIssue + 256 * kRegsSoftmax <= 96 * kThreads, "register shares");
 
 constexpr int kRows = 256;                      // rows a unit
@@ -261,7 +261,7 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
                 low = max(0, rq.ctx + least - A.window + 1);
             }
             const unsigned char* head = A.pool.base + g.h * A.pool.head_stride + (isv ? Blk::v_codes(P) : 0);
-            // The page of tile k's token: looked up (load_page) two tiles ahead and
+            // The page of tile k's token: looked up (load_page) a tile ahead and
             // judged (page_of) only when the codes are fetched, so that nothing waits
             // for the table.
             struct Page {
@@ -327,17 +327,15 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
                 if (lane == 0) mbar_arrive(isv ? &bars.v_full[buf] : &bars.k_full[buf]);
                 ++done;
             };
-            Raw a, z;
-            Page p0 = load_page(0), p1 = load_page(1);
-            fetch(a, 0, page_of(p0));
-            for (int k = 0; k < g.tiles; k += 2) {
-                p0 = load_page(k + 2);
-                if (k + 1 < g.tiles) fetch(z, k + 1, page_of(p1));
+            Raw a;
+            Page next = load_page(0);
+            fetch(a, 0, page_of(next));
+            next = load_page(1);
+#pragma unroll 1
+            for (int k = 0; k < g.tiles; ++k) {
                 put(a);
-                if (k + 1 >= g.tiles) break;
-                p1 = load_page(k + 3);
-                if (k + 2 < g.tiles) fetch(a, k + 2, page_of(p0));
-                put(z);
+                if (k + 1 < g.tiles) fetch(a, k + 1, page_of(next));
+                next = load_page(k + 2);
             }
         }
     } else if (warp >= kMmaWarp) {
