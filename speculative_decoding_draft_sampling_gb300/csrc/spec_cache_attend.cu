@@ -119,7 +119,7 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
     __shared__ uint32_t s_there[kS];            // which page blocks of a stage's tile are there
     __shared__ unsigned long long s_seen[kRows];
     __shared__ float s_max[kAtWarps][kRows];
-    __shared__ float s_l[kAtWarps][kRows], s_lr[kRows];
+    __shared__ float s_l[kAtWarps][kRows], s_lr[kAtWarps][kRows];
     __shared__ int s_last, s_dead;
 
     const int tid = threadIdx.x, lane = tid & 31;
@@ -262,20 +262,14 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
                 for (int nt = 0; nt < NT; ++nt) lds(qf[ks][nt], q_base + ((ks * NT + nt) * 32 + lane) * 8);
         }
 
-        // The sums of rounded weights are a row of ones times P^T; warp w keeps
-        // those of the column blocks w, w + 4, ...
-        constexpr int kLR = (NT + 3) / 4;
-        float o[kMT][NT][4], m[NT][2], l[NT][2], lr[kLR][4];
+        float o[kMT][NT][4], m[NT][2], l[NT][2], lr[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             m[nt][0] = m[nt][1] = kNoMax;
-            l[nt][0] = l[nt][1] = 0.0f;
+            l[nt][0] = l[nt][1] = lr[nt][0] = lr[nt][1] = 0.0f;
 #pragma unroll
             for (int j = 0; j < kMT; ++j) o[j][nt][0] = o[j][nt][1] = o[j][nt][2] = o[j][nt][3] = 0.0f;
         }
-
-#pragma unroll
-        for (int q = 0; q < kLR; ++q) lr[q][0] = lr[q][1] = lr[q][2] = lr[q][3] = 0.0f;
 
         // ---- the tiles -------------------------------------------------------
         int s = 0, refill = kS - 1;             // this tile's stage, the one before it
@@ -361,12 +355,13 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
                 // Weights under the maximum so far, as the 16 x 8 operand P^T.
                 // They are rounded to bf16 for the tensor cores (2^-8 each at
                 // most, as the output's own rounding); lse takes their sum
-                // before that, the output is divided by the sum of the rounded
-                // ones, so that what rounding they have in common cancels (one
-                // dominant key: all of it).  A tile with masked keys, where a
+                // before that (l), the output is divided by the sum of the rounded
+                // ones (lr), so that what rounding they have in common cancels
+                // (one dominant key: all of it).  lr from a row of ones as another
+                // row of V^T cost up to 6 % more.  A tile with masked keys, where a
                 // row may see only a few, adds a second term with what rounding
                 // took from the first.
-                float ls[NT][2];
+                float ls[NT][2], lrs[NT][2];
                 auto weights = [&]() {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
@@ -377,11 +372,15 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
                         ls[nt][1] = p[1] + p[3];
                         const uint32_t ab = pack_bf16(p[0], p[1]), cd = pack_bf16(p[2], p[3]);
                         sts64(pbuf + ((warp * NT + nt) * 32 + lane) * 8, transpose8x8(ab), transpose8x8(cd));
+                        lrs[nt][0] = __uint_as_float(ab << 16) + __uint_as_float(cd << 16);
+                        lrs[nt][1] = __uint_as_float(ab & 0xffff0000u) + __uint_as_float(cd & 0xffff0000u);
                         if constexpr (kMasked) {
                             const uint32_t rab = pack_bf16(p[0] - __uint_as_float(ab << 16),
                                                            p[1] - __uint_as_float(ab & 0xffff0000u));
                             const uint32_t rcd = pack_bf16(p[2] - __uint_as_float(cd << 16),
                                                            p[3] - __uint_as_float(cd & 0xffff0000u));
+                            lrs[nt][0] += __uint_as_float(rab << 16) + __uint_as_float(rcd << 16);
+                            lrs[nt][1] += __uint_as_float(rab & 0xffff0000u) + __uint_as_float(rcd & 0xffff0000u);
                             sts64(lo_base + ((warp * NT + nt) * 32 + lane) * 8, transpose8x8(rab), transpose8x8(rcd));
                         }
                     }
@@ -416,7 +415,7 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
                             const float f = exp2_fast(m[nt][e] - mn);
                             m[nt][e] = mn;
                             l[nt][e] *= f;
-                            if ((nt & 3) == warp) lr[nt >> 2][e] *= f;
+                            lr[nt][e] *= f;
 #pragma unroll
                             for (int j = 0; j < kMT; ++j) {
                                 o[j][nt][e] *= f;
@@ -428,11 +427,12 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
                 }
                 // every warp is past the tile before this one: its stage is free
                 if (warp == ((k - 1 + kS) & 3) && k > 0 && k - 1 + kS < tiles && !s_dead) issue(g, k - 1 + kS, refill);
-                const uint32_t ones[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     l[nt][0] += ls[nt][0];
                     l[nt][1] += ls[nt][1];
+                    lr[nt][0] += lrs[nt][0];
+                    lr[nt][1] += lrs[nt][1];
                 }
                 // O^T += V^T P^T: this warp's rows, all tokens
                 uint32_t vscale;
@@ -471,12 +471,10 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
                         lds(p2, pbuf + ((mb * NT + nt) * 32 + lane) * 8);
 #pragma unroll
                         for (int j = 0; j < kMT; ++j) mma(o[j][nt], a[j], p2[0], p2[1]);
-                        if ((nt & 3) == warp) mma(lr[nt >> 2], ones, p2[0], p2[1]);
                         if constexpr (kMasked) {
                             lds(p2, lo_base + ((mb * NT + nt) * 32 + lane) * 8);
 #pragma unroll
                             for (int j = 0; j < kMT; ++j) mma(o[j][nt], a[j], p2[0], p2[1]);
-                            if ((nt & 3) == warp) mma(lr[nt >> 2], ones, p2[0], p2[1]);
                         }
                     }
                 }
@@ -498,7 +496,11 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
                 t += __shfl_xor_sync(0xffffffffu, t, 8);
                 t += __shfl_xor_sync(0xffffffffu, t, 16);
                 if (r8 == 0) s_l[warp][nt * 8 + 2 * c4 + e] = t;
-                if (r8 == 0 && (nt & 3) == warp) s_lr[nt * 8 + 2 * c4 + e] = lr[nt >> 2][e];
+                t = lr[nt][e];
+                t += __shfl_xor_sync(0xffffffffu, t, 4);
+                t += __shfl_xor_sync(0xffffffffu, t, 8);
+                t += __shfl_xor_sync(0xffffffffu, t, 16);
+                if (r8 == 0) s_lr[warp][nt * 8 + 2 * c4 + e] = t;
             }
         __syncthreads();
         // every warp is past its last tile: the next segment may begin
@@ -531,7 +533,9 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
             for (int e = 0; e < 2; ++e) {
                 const int row = nt * 8 + 2 * c4 + e;
                 float sum = 0.0f, v[2 * kMT];
-                const float rsum = s_lr[row];
+                float rsum = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kAtWarps; ++w) rsum += s_lr[w][row];
 #pragma unroll
                 for (int w = 0; w < kAtWarps; ++w) sum += s_l[w][row];
 #pragma unroll
