@@ -16,9 +16,11 @@
 // rounds to the integer.  Likewise max|x| / 7 is a five-bit tie or at least
 // 1/(7 * 64) of it away from one, and is rounded to 13 bits first.
 //
-// Append and read move 4 bytes of codes or 16 of values a thread with several
-// heads in flight.  Both are bound by HBM on prompts: 8 prompts of 8192 tokens,
-// 8 heads of 128 (268 MB of bf16, 75 MB of cache).
+// Append and read move 4 bytes of codes or 16 of values a thread with four heads
+// in flight.  Both are bound by HBM on prompts: 8 of 8192 tokens, 8 heads of 128
+// (268 MB of bf16, 75 MB of cache), take 68 us to append (5.1 TB/s) and 56 to read
+// (6.1).  Eight heads in flight cost 8 % more, two 3 %, and so do registers cut for
+// more warps an SM: HBM wants long runs from few places at once.
 #include <cuda_bf16.h>
 
 #include "../../include/spec_cache.h"
@@ -28,7 +30,8 @@ namespace spec {
 
 namespace {
 
-constexpr int kRowThreads = 256;
+// Append, then read of those prompts: 107 us at 64 or 128 threads, 111 at 256, 117 at 512.
+constexpr int kRowThreads = 128;
 
 // Eight bf16 of a row into registers, as four words.
 template <bool kAligned>
@@ -105,7 +108,7 @@ __device__ __forceinline__ uint32_t quantise8(uint4 x, uint32_t& scale, bool& ba
     return __byte_perm(__byte_perm(two[0], two[1], 0x0040), __byte_perm(two[2], two[3], 0x0040), 0x5410);
 }
 
-// How the rows are dealt out: blockIdx.x takes 8 (D = 128) or 16 tokens,
+// How the rows are dealt out: blockIdx.x takes 4 (D = 128) or 8 tokens,
 // blockIdx.y a request, blockIdx.z a range of heads; D/8 threads take K or V of
 // one token and go through the heads, four at a time.
 template <int D>
@@ -234,7 +237,7 @@ dim3 row_grid(const CacheRowsArgs& A, int& heads_per) {
     const int x = (A.n + RowPlace<D>::kTokens - 1) / RowPlace<D>::kTokens, y = A.B < 65535 ? A.B : 65535;
     const long long blocks = static_cast<long long>(x) * y;
     heads_per = A.pool.heads;
-    if (blocks < 608 && heads_per > kFly) heads_per = kFly;
+    if (blocks < 1216 && heads_per > kFly) heads_per = kFly;
     const int z = (A.pool.heads + heads_per - 1) / heads_per;
     return dim3(static_cast<unsigned>(x), static_cast<unsigned>(y), static_cast<unsigned>(z));
 }
