@@ -103,9 +103,10 @@ spec_status spec_cache_read(
  * Outputs: out bf16 [B, n, q_heads, D] contiguous: softmax over the seen keys
  *   times V; lse NULL or fp32 [B, n, q_heads]: natural log of the softmax's
  *   denominator.  Rows that see nothing, and rows i >= num_rows[b], are 0 with
- *   lse = -inf.  Keys that no row sees contribute nothing whatever the cache
- *   holds there.  Scales of seen positions must be finite, as
- *   spec_cache_append writes them.
+ *   lse = -inf.  Positions past the last drafted row, and context that lies
+ *   outside every row's window, contribute nothing whatever the cache holds
+ *   there.  Scales of all other positions must be finite, as spec_cache_append
+ *   writes them.
  *   ws       sized by the query for the same shape, 16-byte aligned; its first
  *            SPEC_CACHE_WS_CONTROL bytes must be zero before the first call
  *            and are zero again after every call (except the error word that

