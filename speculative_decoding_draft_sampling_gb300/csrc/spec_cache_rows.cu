@@ -17,10 +17,11 @@
 // 1/(7 * 64) of it away from one, and is rounded to 13 bits first.
 //
 // Append and read move 4 bytes of codes or 16 of values a thread with four heads
-// in flight.  Both are bound by HBM on prompts: 8 of 8192 tokens, 8 heads of 128
-// (268 MB of bf16, 75 MB of cache), take 68 us to append (5.1 TB/s) and 56 to read
-// (6.1).  Eight heads in flight cost 8 % more, two 3 %, and so do registers cut for
-// more warps an SM: HBM wants long runs from few places at once.
+// in flight.  8 prompts of 8192 tokens, 8 heads of 128 (268 MB of bf16, 75 MB of
+// cache), take 64 us to append (5.4 TB/s) and 56 to read (6.1).  Reading is bound by
+// HBM; writing by its instructions as well (four fifths of the issue slots), so its
+// products come in pairs and its addresses by steps (68 us before).  Eight heads in
+// flight cost 8 % more, two 3 %; registers cut for more warps an SM cost 8 % too.
 #include <cuda_bf16.h>
 
 #include "../../include/spec_cache.h"
@@ -30,7 +31,8 @@ namespace spec {
 
 namespace {
 
-// Append, then read of those prompts: 107 us at 64 or 128 threads, 111 at 256, 117 at 512.
+// Append, then read of those prompts: 105 us at 128 threads; at 64 the same, at 256 4 us
+// more, at 512 10.
 constexpr int kRowThreads = 128;
 
 // Eight bf16 of a row into registers, as four words.
@@ -54,9 +56,17 @@ __device__ __forceinline__ float scale_of(float top) {
     return u < 0x03800000u ? 0.0f : __uint_as_float(u);
 }
 
-// an integer whose low four bits are the code of x under a scale of reciprocal r
-__device__ __forceinline__ uint32_t code_of(float x, float r) {
-    return __float_as_uint(__fadd_rn(__fmaf_rn(x, r, 1536.0f), 12582912.0f + 8.0f - 1536.0f));
+// Two neighbours' codes under a scale of reciprocal r, in the low byte: each result
+// is an integer whose low four bits are a code.
+__device__ __forceinline__ uint32_t codes_of(uint32_t w, float r) {
+    unsigned long long x, y;
+    asm("{\n\t.reg .b64 a, c;\n\tmov.b64 a, {%2, %2};\n\tmov.b64 c, {%3, %3};\n\t"
+        "mov.b64 %0, {%4, %5};\n\tfma.rn.f32x2 %0, %0, a, c;\n\t"
+        "mov.b64 c, {%6, %6};\n\tadd.rn.f32x2 %1, %0, c;\n\t}"
+        : "=&l"(x), "=l"(y)
+        : "f"(r), "f"(1536.0f), "f"(__uint_as_float(w << 16)), "f"(__uint_as_float(w & 0xffff0000u)),
+          "f"(12582912.0f + 8.0f - 1536.0f));
+    return static_cast<uint32_t>(y >> 32) * 16u + static_cast<uint32_t>(y);
 }
 
 // Quantises a thread's eight values (four neighbouring lanes share a group, the
@@ -103,8 +113,7 @@ __device__ __forceinline__ uint32_t quantise8(uint4 x, uint32_t& scale, bool& ba
     if (s == 0.0f) r = 0.0f;
     uint32_t two[4];                                        // low byte: the codes of two neighbours
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        two[i] = code_of(__uint_as_float(w[i] & 0xffff0000u), r) * 16u + code_of(__uint_as_float(w[i] << 16), r);
+    for (int i = 0; i < 4; ++i) two[i] = codes_of(w[i], r);
     return __byte_perm(__byte_perm(two[0], two[1], 0x0040), __byte_perm(two[2], two[3], 0x0040), 0x5410);
 }
 
@@ -142,17 +151,20 @@ __global__ void __launch_bounds__(kRowThreads) cache_append_kernel(const CacheRo
             pos = static_cast<long long>(A.start[b]) + at.i;
             page = cache_page(A.tab, A.pool.num_pages, A.pool.p_shift, b, pos);
         }
-        const uint16_t* src = at.isv ? A.v + b * A.v_bs + at.i * A.v_rs + c * 8 : A.k + b * A.k_bs + at.i * A.k_rs + c * 8;
         const long long hs = at.isv ? A.v_hs : A.k_hs;
+        const uint16_t* src = (at.isv ? A.v + b * A.v_bs + at.i * A.v_rs : A.k + b * A.k_bs + at.i * A.k_rs) + h0 * hs + c * 8;
         const int slot = static_cast<int>(pos & (P - 1));
-        unsigned char* blk = A.pool.base + page * A.pool.page_stride + (at.isv ? Blk::v_codes(P) : 0);
+        // this thread's codes and, P rows of codes on, its row's scales
+        unsigned char* to = A.pool.base + page * A.pool.page_stride + h0 * A.pool.head_stride + (at.isv ? Blk::v_codes(P) : 0);
+        unsigned char* to_s = to + P * Blk::kRow + slot * Blk::kScl + (c >> 2) * 2;
+        to += slot * Blk::kRow + c * 4;
         bool bad = false;
-        for (int h = h0; h < h1; h += kFly) {
+        for (int h = h0; h < h1; h += kFly, src += kFly * hs, to += kFly * A.pool.head_stride, to_s += kFly * A.pool.head_stride) {
             uint4 x[kFly];
 #pragma unroll
             for (int q = 0; q < kFly; ++q) {
                 x[q] = make_uint4(0, 0, 0, 0);
-                if (live && h + q < h1) x[q] = load8<kAligned>(src + (h + q) * hs);
+                if (live && h + q < h1) x[q] = load8<kAligned>(src + q * hs);
             }
 #pragma unroll
             for (int q = 0; q < kFly; ++q) {
@@ -160,10 +172,9 @@ __global__ void __launch_bounds__(kRowThreads) cache_append_kernel(const CacheRo
                 uint32_t scale;
                 const uint32_t codes = quantise8(x[q], scale, bad);
                 if (page >= 0) {
-                    unsigned char* to = blk + (h + q) * A.pool.head_stride;
-                    reinterpret_cast<uint32_t*>(to + slot * Blk::kRow)[c] = codes;
+                    *reinterpret_cast<uint32_t*>(to + q * A.pool.head_stride) = codes;
                     if ((c & 3) == 0)
-                        reinterpret_cast<uint16_t*>(to + P * Blk::kRow + slot * Blk::kScl)[c >> 2] = static_cast<uint16_t>(scale);
+                        *reinterpret_cast<uint16_t*>(to_s + q * A.pool.head_stride) = static_cast<uint16_t>(scale);
                 }
             }
         }
