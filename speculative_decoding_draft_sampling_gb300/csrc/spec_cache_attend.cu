@@ -150,6 +150,7 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
         s_dead = 0;
     }
 
+    after_earlier();
     Share<kTile, kAtWarps> share(A, L, s_share, kRows);
     if (share.lo() == share.hi()) return;
     const int cta = blockIdx.x;
@@ -699,8 +700,7 @@ cudaError_t attend(const CacheAttendArgs& A, cudaStream_t st) {
         if (e != cudaSuccess) return e;
         if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
-    cache_attend_kernel<D, NT><<<grid, kAtThreads, Cfg::kSmem, st>>>(A, L);
-    return cudaGetLastError();
+    return launch_early(cache_attend_kernel<D, NT>, grid, kAtThreads, Cfg::kSmem, st, A, L);
 }
 
 template <int D>

@@ -168,6 +168,12 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
         : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
     return r;
 }
+// a load that stays where it stands
+__device__ __forceinline__ uint32_t ld_now_u32(const void* p) {
+    uint32_t v;
+    asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
 // where piece j (8 elements, 16 bytes) of row r lies in such a matrix
 __device__ __forceinline__ uint32_t piece_at(int r, int j) {
     return (j >> 3) * kChunk + r * 128 + (((j & 7) ^ (r & 7)) << 4);
@@ -210,6 +216,7 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t v_buf = base, k_buf = base + 2 * kTile, q_buf = base + 4 * kTile;
 
+    after_earlier();
     Share<kTok, kWarps> share(A, L, s_share, kRows);
     if (share.lo() == share.hi()) return;
     if (tid == 0) {
@@ -282,7 +289,7 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
                 const int at = rq.real(g.v0 + k) * kTok + t;
                 p.wanted = rq.needs(A, at, at + 1) && !(A.window > 0 && at < low && at >= A.sinks);
                 if (p.wanted && (at >> p_shift) < A.tab.width)
-                    p.id = static_cast<int>(ldg_now_u32(A.tab.table + g.b * A.tab.stride + (at >> p_shift)));
+                    p.id = static_cast<int>(ld_now_u32(A.tab.table + g.b * A.tab.stride + (at >> p_shift)));
                 return p;
             };
             auto page_of = [&](const Page& p) {
@@ -305,15 +312,15 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
                 const uint4* c = reinterpret_cast<const uint4*>(blk + slot * Blk::kRow);
 #pragma unroll
                 for (int i = 0; i < kW / 4; ++i) {
-                    const uint4 x = __ldg(c + i);
+                    const uint4 x = c[i];
                     r.w[4 * i] = x.x; r.w[4 * i + 1] = x.y; r.w[4 * i + 2] = x.z; r.w[4 * i + 3] = x.w;
                 }
                 const unsigned char* s = blk + P * Blk::kRow + slot * Blk::kScl;
                 if constexpr (D == 128) {
-                    const uint2 x = __ldg(reinterpret_cast<const uint2*>(s));
+                    const uint2 x = *reinterpret_cast<const uint2*>(s);
                     r.s[0] = x.x; r.s[1] = x.y;
                 } else {
-                    r.s[0] = __ldg(reinterpret_cast<const uint32_t*>(s));
+                    r.s[0] = *reinterpret_cast<const uint32_t*>(s);
                 }
             };
             auto put = [&](const Raw& r) {
@@ -457,7 +464,7 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
                 for (int j = 0; j < D / 8; ++j) {
                     uint4 x;
                     if (A.aligned) {
-                        x = __ldg(reinterpret_cast<const uint4*>(q + 8 * j));
+                        x = *reinterpret_cast<const uint4*>(q + 8 * j);
                     } else {
                         uint32_t y[4];
 #pragma unroll
@@ -488,7 +495,7 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
             auto page_at = [&](int at) {
                 if (!rq.needs(A, at, at + P)) return 0;
                 return (at >> p_shift) < A.tab.width
-                           ? static_cast<int>(ldg_now_u32(A.tab.table + g.b * A.tab.stride + (at >> p_shift)))
+                           ? static_cast<int>(ld_now_u32(A.tab.table + g.b * A.tab.stride + (at >> p_shift)))
                            : -1;
             };
             bool missing = false;
@@ -814,8 +821,7 @@ cudaError_t attend_tc(const CacheAttendArgs& A, cudaStream_t st) {
         if (e != cudaSuccess) return e;
         if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
-    cache_attend_tc_kernel<D><<<grid, kThreads, Cfg::kSmem, st>>>(A, L);
-    return cudaGetLastError();
+    return launch_early(cache_attend_tc_kernel<D>, grid, kThreads, Cfg::kSmem, st, A, L);
 }
 
 }  // namespace

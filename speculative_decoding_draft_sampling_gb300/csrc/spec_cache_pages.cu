@@ -62,6 +62,7 @@ __device__ __forceinline__ int stack_size(const CachePagesArgs& A) {
 }
 
 __global__ void __launch_bounds__(kPageThreads) cache_reserve_kernel(const CachePagesArgs A) {
+    after_earlier();
     __shared__ int sums[kPageWarps];
     __shared__ int4 grant[kPageThreads];        // a request's pages: first of the taken, where in its row, how many
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -108,6 +109,7 @@ __global__ void __launch_bounds__(kPageThreads) cache_reserve_kernel(const Cache
 // References first, then the pages that nothing holds any more, marked in a
 // bitmap in shared memory: reading it in order gives the stack its order.
 __global__ void __launch_bounds__(kPageThreads) cache_release_kernel(const CachePagesArgs A) {
+    after_earlier();
     extern __shared__ uint32_t freed[];         // one bit a page
     __shared__ int sums[kPageWarps];
     __shared__ int2 spans[kPageThreads];
@@ -182,6 +184,8 @@ __global__ void __launch_bounds__(kPageThreads) cache_release_kernel(const Cache
 }
 
 __global__ void __launch_bounds__(kPageThreads) cache_fork_kernel(const CachePagesArgs A) {
+    after_earlier();
+    let_next_start();                           // the copy
     __shared__ int sums[kPageWarps];
     __shared__ int4 shares[kPageThreads];       // parent, child, full pages shared
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -248,7 +252,7 @@ template <int D>
 __global__ void __launch_bounds__(kCopyThreads) cache_copy_kernel(const CachePagesArgs A) {
     using Blk = CacheBlock<D>;
     using Scl = typename std::conditional<D == 128, uint2, uint32_t>::type;    // a row's scales
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    after_earlier();
     const int f = blockIdx.y, P = A.pool.P;
     const int to = A.new_page[f];
     if (to < 0) return;
@@ -296,8 +300,7 @@ __global__ void __launch_bounds__(kCopyThreads) cache_copy_kernel(const CachePag
 }  // namespace
 
 cudaError_t cache_reserve_run(const CachePagesArgs& A, cudaStream_t st) {
-    cache_reserve_kernel<<<1, kPageThreads, 0, st>>>(A);
-    return cudaGetLastError();
+    return launch_early(cache_reserve_kernel, 1, kPageThreads, 0, st, A);
 }
 
 cudaError_t cache_release_run(const CachePagesArgs& A, cudaStream_t st) {
@@ -307,27 +310,16 @@ cudaError_t cache_release_run(const CachePagesArgs& A, cudaStream_t st) {
                                                    kCacheMaxPages / 8);
         if (e != cudaSuccess) return e;
     }
-    cache_release_kernel<<<1, kPageThreads, smem, st>>>(A);
-    return cudaGetLastError();
+    return launch_early(cache_release_kernel, 1, kPageThreads, smem, st, A);
 }
 
 cudaError_t cache_fork_run(const CachePagesArgs& A, cudaStream_t st) {
-    cache_fork_kernel<<<1, kPageThreads, 0, st>>>(A);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_early(cache_fork_kernel, 1, kPageThreads, 0, st, A);
     if (e != cudaSuccess) return e;
     // the copy waits for the decisions on the device, not for their launch's end
     const int pairs = A.pool.layers * A.pool.heads;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((pairs + kBlocks - 1) / kBlocks), static_cast<unsigned>(A.F));
-    cfg.blockDim = dim3(kCopyThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return A.pool.D == 128 ? cudaLaunchKernelEx(&cfg, cache_copy_kernel<128>, A)
-                           : cudaLaunchKernelEx(&cfg, cache_copy_kernel<64>, A);
+    const dim3 grid(static_cast<unsigned>((pairs + kBlocks - 1) / kBlocks), static_cast<unsigned>(A.F));
+    return launch_early(A.pool.D == 128 ? cache_copy_kernel<128> : cache_copy_kernel<64>, grid, kCopyThreads, 0, st, A);
 }
 
 }  // namespace spec

@@ -139,6 +139,7 @@ constexpr int kFly = 4;                                     // heads in flight
 // Every thread of a warp takes part in the shuffles, live or not.
 template <int D, bool kAligned>
 __global__ void __launch_bounds__(kRowThreads) cache_append_kernel(const CacheRowsArgs A, int heads_per) {
+    after_earlier();
     using Blk = CacheBlock<D>;
     const RowPlace<D> at;
     const int c = at.c, P = A.pool.P;
@@ -200,6 +201,7 @@ __device__ __forceinline__ uint4 values8(uint32_t w, uint32_t s2, uint32_t c2) {
 
 template <int D>
 __global__ void __launch_bounds__(kRowThreads) cache_read_kernel(const CacheRowsArgs A, int heads_per) {
+    after_earlier();
     using Blk = CacheBlock<D>;
     const RowPlace<D> at;
     const int c = at.c, P = A.pool.P, H = A.pool.heads;
@@ -259,26 +261,24 @@ cudaError_t cache_append_run(const CacheRowsArgs& A, cudaStream_t st) {
     int per;
     if (A.pool.D == 128) {
         const dim3 grid = row_grid<128>(A, per);
-        if (A.aligned) cache_append_kernel<128, true><<<grid, kRowThreads, 0, st>>>(A, per);
-        else cache_append_kernel<128, false><<<grid, kRowThreads, 0, st>>>(A, per);
+        if (A.aligned) return launch_early(cache_append_kernel<128, true>, grid, kRowThreads, 0, st, A, per);
+        else return launch_early(cache_append_kernel<128, false>, grid, kRowThreads, 0, st, A, per);
     } else {
         const dim3 grid = row_grid<64>(A, per);
-        if (A.aligned) cache_append_kernel<64, true><<<grid, kRowThreads, 0, st>>>(A, per);
-        else cache_append_kernel<64, false><<<grid, kRowThreads, 0, st>>>(A, per);
+        if (A.aligned) return launch_early(cache_append_kernel<64, true>, grid, kRowThreads, 0, st, A, per);
+        else return launch_early(cache_append_kernel<64, false>, grid, kRowThreads, 0, st, A, per);
     }
-    return cudaGetLastError();
 }
 
 cudaError_t cache_read_run(const CacheRowsArgs& A, cudaStream_t st) {
     int per;
     if (A.pool.D == 128) {
         const dim3 grid = row_grid<128>(A, per);
-        cache_read_kernel<128><<<grid, kRowThreads, 0, st>>>(A, per);
+        return launch_early(cache_read_kernel<128>, grid, kRowThreads, 0, st, A, per);
     } else {
         const dim3 grid = row_grid<64>(A, per);
-        cache_read_kernel<64><<<grid, kRowThreads, 0, st>>>(A, per);
+        return launch_early(cache_read_kernel<64>, grid, kRowThreads, 0, st, A, per);
     }
-    return cudaGetLastError();
 }
 
 // ---------------------------------------------------------------------------
@@ -299,6 +299,7 @@ constexpr int kCompactBatch = 8;                // rows whose loads are in fligh
 // 13 us, 2.4 TB/s in pieces of 16 and 8 bytes; 4 requests of 4 layers 4 us.
 template <int D>
 __global__ void __launch_bounds__(kCompactThreads) cache_compact_kernel(const CacheCompactArgs A, int pairs_per_cta) {
+    after_earlier();
     extern __shared__ int2 moves[];             // (page * P + slot) from, to
     __shared__ int count;
     using Blk = CacheBlock<D>;
@@ -387,9 +388,8 @@ cudaError_t cache_compact_run(const CacheCompactArgs& A, cudaStream_t st) {
     const int per = max(1, kCompactThreads / kPieces);
     const dim3 grid(static_cast<unsigned>((pairs + per - 1) / per), static_cast<unsigned>(A.B));
     const size_t smem = static_cast<size_t>(A.path_width) * sizeof(int2);
-    if (A.pool.D == 128) cache_compact_kernel<128><<<grid, kCompactThreads, smem, st>>>(A, per);
-    else cache_compact_kernel<64><<<grid, kCompactThreads, smem, st>>>(A, per);
-    return cudaGetLastError();
+    if (A.pool.D == 128) return launch_early(cache_compact_kernel<128>, grid, kCompactThreads, smem, st, A, per);
+    else return launch_early(cache_compact_kernel<64>, grid, kCompactThreads, smem, st, A, per);
 }
 
 }  // namespace spec
