@@ -24,12 +24,12 @@
 // 128 tokens halve the barriers, but their registers cost a CTA an SM: slower.)
 //
 // What bounds it.  Up to 8 rows: turning codes into bf16, near half of a tile's
-// instructions (4 requests of 131072 tokens, 8 heads of 128, 4 rows a head: 127 us,
-// 3.4 TB/s of cache, 69 % of the issue slots).  From 16 rows on the tensor
+// instructions (4 requests of 131072 tokens, 8 heads of 128, 4 rows a head: 124 us,
+// 3.5 TB/s of cache, 69 % of the issue slots).  From 16 rows on the tensor
 // instruction itself: a scheduler takes one in 8 cycles, 16 for every 8 rows of a tile
-// and warp (256 requests of 4096 tokens, 36 rows a head: 448 us, 216 TFLOP/s, those
+// and warp (256 requests of 4096 tokens, 36 rows a head: 445 us, 218 TFLOP/s, those
 // cycles are 68 % of all).
-// One request of a few hundred tokens takes 12 us: launch, the deal of the work, one
+// One request of a few hundred tokens takes 10 us: launch, the deal of the work, one
 // tile, the join.
 #include <atomic>
 #include <type_traits>

@@ -18,9 +18,9 @@
 //
 // Append and read move 4 bytes of codes or 16 of values a thread with four heads
 // in flight.  8 prompts of 8192 tokens, 8 heads of 128 (268 MB of bf16, 75 MB of
-// cache), take 64 us to append (5.4 TB/s) and 56 to read (6.1).  Reading is bound by
+// cache), take 62 us to append (5.5 TB/s) and 55 to read (6.3).  Reading is bound by
 // HBM; writing by its instructions as well (four fifths of the issue slots), so its
-// products come in pairs and its addresses by steps (68 us before).  Eight heads in
+// products come in pairs and its addresses by steps (4 us).  Eight heads in
 // flight cost 8 % more, two 3 %; registers cut for more warps an SM cost 8 % too.
 #include <cuda_bf16.h>
 
@@ -31,7 +31,7 @@ namespace spec {
 
 namespace {
 
-// Append, then read of those prompts: 105 us at 128 threads; at 64 the same, at 256 4 us
+// Append, then read of those prompts: 100 us at 128 threads; at 64 the same, at 256 4
 // more, at 512 10.
 constexpr int kRowThreads = 128;
 
@@ -296,7 +296,7 @@ constexpr int kCompactBatch = 8;                // rows whose loads are in fligh
 // batches in order, the copy is right in place, and threads never meet.
 // Its time is a chain of three dependent reads (path, page, row) and a store, not
 // bytes: 128 requests of 32 layers and 8 heads of 128, trees of 64 (31 MB moved), take
-// 13 us, 2.4 TB/s in pieces of 16 and 8 bytes; 4 requests of 4 layers 4 us.
+// 11 us, 2.8 TB/s in pieces of 16 and 8 bytes; 4 requests of 4 layers 3 us.
 template <int D>
 __global__ void __launch_bounds__(kCompactThreads) cache_compact_kernel(const CacheCompactArgs A, int pairs_per_cta) {
     after_earlier();
