@@ -59,12 +59,11 @@ __device__ __forceinline__ float scale_of(float top) {
 // Two neighbours' codes under a scale of reciprocal r, in the low byte: each result
 // is an integer whose low four bits are a code.
 __device__ __forceinline__ uint32_t codes_of(uint32_t w, float r) {
-    unsigned long long x, y;
-    asm("{\n\t.reg .b64 a, c;\n\tmov.b64 a, {%2, %2};\n\tmov.b64 c, {%3, %3};\n\t"
-        "mov.b64 %0, {%4, %5};\n\tfma.rn.f32x2 %0, %0, a, c;\n\t"
-        "mov.b64 c, {%6, %6};\n\tadd.rn.f32x2 %1, %0, c;\n\t}"
-        : "=&l"(x), "=l"(y)
-        : "f"(r), "f"(1536.0f), "f"(__uint_as_float(w << 16)), "f"(__uint_as_float(w & 0xffff0000u)),
+    unsigned long long y;
+    asm("{\n\t.reg .b64 x, a, c;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 a, {%3, %3};\n\tmov.b64 c, {%4, %4};\n\t"
+        "fma.rn.f32x2 x, x, a, c;\n\tmov.b64 c, {%5, %5};\n\tadd.rn.f32x2 %0, x, c;\n\t}"
+        : "=l"(y)
+        : "f"(__uint_as_float(w << 16)), "f"(__uint_as_float(w & 0xffff0000u)), "f"(r), "f"(1536.0f),
           "f"(12582912.0f + 8.0f - 1536.0f));
     return static_cast<uint32_t>(y >> 32) * 16u + static_cast<uint32_t>(y);
 }
