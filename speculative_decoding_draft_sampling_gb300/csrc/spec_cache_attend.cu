@@ -126,7 +126,10 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
     __shared__ uint64_t full[kS];
     __shared__ ShareScratch<kAtWarps> s_share;
     __shared__ long long s_out[kRows];          // a row's place in out and lse (-1: none)
-    __shared__ uint32_t s_there[kS];            // which page blocks of a stage's tile are there
+    // which page blocks of a stage's tile are there; above them, once copies into the
+    // stage were given out, kGiven and the parity that their barrier's wait takes
+    constexpr uint32_t kThere = 0xfu, kGiven = 0x10u, kParity = 5;
+    __shared__ uint32_t s_there[kS];
     __shared__ unsigned long long s_seen[kRows];
     __shared__ float s_max[kAtWarps][kRows];
     __shared__ float s_l[kAtWarps][kRows], s_lr[kAtWarps][kRows];
@@ -145,7 +148,10 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
 
     if (tid == 0) {
 #pragma unroll
-        for (int s = 0; s < kS; ++s) mbar_init(&full[s], 1);
+        for (int s = 0; s < kS; ++s) {
+            mbar_init(&full[s], 1);
+            s_there[s] = 0;
+        }
         fence_mbar_init();
         s_dead = 0;
     }
@@ -194,7 +200,7 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
         if (g_test_drop && cta == 0 && k == 0) return;
 #endif
         if (lane == 0) {
-            s_there[s] = there;
+            s_there[s] = there | kGiven | (phases >> s & 1u) << kParity;
             mbar_expect_tx(&full[s], __popc(there) * Blk::bytes(P));
         }
         __syncwarp();
@@ -290,7 +296,7 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
                 s_dead = 1;
                 atomicOr(&L.ctrl->error, SPEC_WS_ERR_WAIT);
             }
-            const uint32_t there = s_there[s];
+            const uint32_t there = s_there[s] & kThere;
             phases ^= 1u << s;
             const uint32_t stage = ring + s * Cfg::kStageBytes;
             const uint32_t pbuf = p_base + (k & 1) * Cfg::kP;
@@ -635,6 +641,8 @@ cache_attend_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_cons
         if (!more) break;
         __syncthreads();                        // shared memory is written again
     }
+    // After a wait that gave up: copies on their way land before the CTA ends.
+    if (s_dead && tid < kS && (s_there[tid] & kGiven)) mbar_wait(&full[tid], s_there[tid] >> kParity & 1u);
 }
 
 }  // namespace

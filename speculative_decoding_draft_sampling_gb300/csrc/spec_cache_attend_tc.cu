@@ -195,6 +195,7 @@ struct TcBars {
     uint64_t s_full[2], p_full[2];              // by S
     uint64_t o_done[2], o_free[2];              // by group: a unit's last product, its O read
     uint64_t q_full, q_empty, pv_done;
+    uint64_t drained;                           // all that the tensor core was given
 };
 
 template <int D>
@@ -233,6 +234,7 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
         mbar_init(&bars.q_full, 8);
         mbar_init(&bars.q_empty, 1);
         mbar_init(&bars.pv_done, 1);
+        mbar_init(&bars.drained, 1);
         fence_mbar_init();
         s_dead = 0;
     }
@@ -437,6 +439,14 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
                 };
                 for (int i = 0; i < jobs + 2; ++i) step(i);
                 tiles_done += g.tiles;
+            }
+            // Products and arrivals on the barriers may still be on their way, those of
+            // roles that gave up among them: tensor memory is freed, and the CTA ends,
+            // only behind this last arrival.
+            if (tiles_done > 0) {
+                if (elect_one()) tc_commit(&bars.drained);
+                __syncwarp();
+                if (!mbar_wait(&bars.drained, 0)) atomicOr(&L.ctrl->error, SPEC_WS_ERR_WAIT);
             }
         }
         __syncwarp();
