@@ -583,7 +583,9 @@ cache_attend_tc_kernel(const __grid_constant__ CacheAttendArgs A, const __grid_c
                             look(y, c + 1);
                         }
                         top *= cs;
-                        if (__any_sync(0xffffffffu, top > m + kSlack)) {
+                        // (rows that are not there multiply what lay in shared memory before:
+                        // they have no say)
+                        if (__any_sync(0xffffffffu, live && top > m + kSlack)) {
                             const float mn = fmaxf(m, top), f = exp2_fast(m - mn);
                             m = mn;
                             l2 = make_float2(l2.x * f, l2.y * f);

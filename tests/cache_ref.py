@@ -127,6 +127,74 @@ def attend(q, pool, table, ctx, rows, mask=None, depth=None, window=0, sinks=0, 
     return out, lse, absv, size
 
 
+def values(pool, which):
+    """All of a pool at once: [pages, heads, P, D] float64."""
+    D, P = pool.D, pool.P
+    a, b = pool.off[which]
+    codes = pool.raw[..., a:a + P * D // 2].reshape(pool.raw.shape[:2] + (P, D // 2))
+    c = np.empty(pool.raw.shape[:2] + (P, D), dtype=np.float64)
+    c[..., 0::2] = codes & 15
+    c[..., 1::2] = codes >> 4
+    s = np.ascontiguousarray(pool.raw[..., b:b + P * D // 16]).view(np.uint16).astype(np.uint32) << 16
+    with np.errstate(invalid="ignore"):           # unwritten scales may be any NaN
+        s = s.view(np.float32).astype(np.float64).reshape(pool.raw.shape[:2] + (P, D // 32))
+        return (c - 8) * np.repeat(s, 32, -1)
+
+
+def seen_rows(ctx, rows, n, mask, depth, window, sinks):
+    """`seen_by` without its loops."""
+    t = np.arange(ctx + rows)
+    i = np.arange(n)
+    d = i if depth is None else np.asarray(depth, dtype=np.int64)
+    j = np.clip(t - ctx, 0, max(n - 1, 0))
+    key = np.where(t < ctx, t, ctx + d[j])
+    if mask is None:
+        own = j[None] <= i[:, None]
+    else:
+        own = (np.asarray(mask).view(np.uint64)[:, j // 64] >> (j % 64).astype(np.uint64)) & np.uint64(1) != 0
+    vis = np.where(t < ctx, True, own) & (i < rows)[:, None]
+    if window > 0:
+        vis &= (ctx + d[:, None] - key[None] < window) | (key < sinks)[None]
+    return vis
+
+
+def attend_many(q, pool, table, ctx, rows, mask=None, depth=None, window=0, sinks=0, scale=None):
+    """`attend` for many rows and long contexts: a kv head's rows at once."""
+    q = q.detach().double().cpu().numpy()
+    B, n, hq, D = q.shape
+    H = pool.raw.shape[1]
+    G = hq // H
+    scale = 1 / math.sqrt(D) if scale is None else scale
+    out, absv = np.zeros((B, n, hq, D)), np.zeros((B, n, hq, D))
+    lse, size = np.full((B, n, hq), -np.inf), np.zeros((B, n, hq))
+    kk, vv = values(pool, "k"), values(pool, "v")
+    for b in range(B):
+        c = max(0, min(int(ctx[b]), table.shape[1] * pool.P))
+        r = n if rows is None else max(0, min(int(rows[b]), n))
+        t = np.arange(c + r)
+        page = np.where(t // pool.P < table.shape[1], table[b][np.minimum(t // pool.P, table.shape[1] - 1)], -1)
+        there = (page >= 0) & (page < pool.raw.shape[0])
+        vis = seen_rows(c, r, n, None if mask is None else mask[b], None if depth is None else depth[b], window, sinks)
+        vis &= there[None]
+        some, used = vis.any(1), vis.any(0)
+        if not some.any():
+            continue
+        page, slot, see = page[used], t[used] % pool.P, vis[some][:, None][..., used]
+        for h in range(H):
+            k, v = kk[page, h, slot], vv[page, h, slot]
+            y = q[b, some, h * G:(h + 1) * G]
+            x = np.where(see, (y @ k.T) * scale, -np.inf)
+            m = x.max(-1, keepdims=True)
+            e = np.exp(x - m)
+            total = e.sum(-1, keepdims=True)
+            at = np.ix_([b], np.nonzero(some)[0], range(h * G, (h + 1) * G))
+            out[at] = (e @ v / total)[None]
+            absv[at] = (e @ np.abs(v) / total)[None]
+            lse[at] = (m + np.log(total))[..., 0][None]
+            size[at] = np.where(see, np.abs(y) @ np.abs(k).T, 0.0).max(-1)[None] * scale
+    return out, lse, absv, size
+
+
 def check_attend(got, lse, ref):
     """out: its own rounding to bf16 (2^-9 of |o|), and the weights' rounding
     to bf16 before they meet V (2^-9 of the weighted |v|), with as much again

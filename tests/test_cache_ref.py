@@ -58,3 +58,33 @@ def test_attend_closed_form():
     q = torch.ones((1, 1, 1, D), dtype=torch.bfloat16)        # keys are 0: all weights equal
     out, lse, _, _ = cache_ref.attend(q, pool, np.zeros((1, 1), dtype=int), [3], None)
     assert np.allclose(out, 7.0 * 2.5) and np.allclose(lse, np.log(4))
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (9, 2), (40, 30)])
+@pytest.mark.parametrize("tree", [False, True])
+def test_attend_many_is_attend(window, sinks, tree):
+    """The form for many rows agrees with the one that goes key by key."""
+    rng = np.random.default_rng(window + tree)
+    D, P, n, H = 64, 16, 70, 2
+    raw = rng.integers(0, 256, (9, H, P * D * 9 // 8), dtype=np.uint8)
+    pool = cache_ref.Pool(torch.from_numpy(raw), D)
+    for page in range(9):
+        for h in range(H):
+            for slot in range(P):
+                for w in "kv":
+                    pool.put(page, h, slot, w, rng.standard_normal(D))
+    table = np.array([[3, 0, 5, 1, 8, 4, 2], [6, 7, -1, 1 << 20, 0, 3, 5]])
+    ctx, rows = [33, 20], [n, 50]
+    mask = depth = None
+    if tree:
+        low = np.tril(rng.integers(0, 2, (2, n, n)), -1) + np.eye(n, dtype=int)
+        mask = np.zeros((2, n, 2), dtype=np.uint64)
+        for j in range(n):
+            mask[:, :, j // 64] |= low[:, :, j].astype(np.uint64) << np.uint64(j % 64)
+        mask, depth = mask.view(np.int64), 3 + rng.integers(0, 20, (2, n)).astype(np.int32)
+    q = torch.from_numpy(rng.standard_normal((2, n, 4, D)))
+    want = cache_ref.attend(q, pool, table, ctx, rows, mask, depth, window, sinks)
+    got = cache_ref.attend_many(q, pool, table, ctx, rows, mask, depth, window, sinks)
+    for a, z in zip(got, want):
+        assert (np.isneginf(a) == np.isneginf(z)).all()
+        assert np.allclose(a, z, rtol=1e-12, atol=1e-12)
