@@ -111,7 +111,9 @@ spec_status spec_cache_read(
  *            SPEC_CACHE_WS_CONTROL bytes must be zero before the first call
  *            and are zero again after every call (except the error word that
  *            spec_workspace_error reads).  One workspace serves calls of any
- *            shape that fits it, one after another.
+ *            shape that fits it, one after another.  A captured graph keeps its
+ *            address: it has to outlive the graph, and nothing else may use it
+ *            while a replay runs.
  * 1 <= n <= 1024.  Deterministic: the same inputs give the same bits.
  * ---------------------------------------------------------------------- */
 size_t spec_cache_attend_workspace_size(int B, int n, int q_heads, int kv_heads, int head_dim);

@@ -62,7 +62,8 @@ def build_binding() -> str:
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I", os.path.join(top, "include"),
            "-I", os.path.join(top, "include", "torch", "csrc", "api", "include"),
            "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"), BINDING_SRC, "-o", tmp,
-           "-L", os.path.join(top, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
+           "-L", os.path.join(top, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cuda", "-lc10", "-lc10_cuda",
+           "-L", os.path.join(cuda, "lib64"), "-lcudart"]
     os.makedirs(LIBDIR, exist_ok=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:

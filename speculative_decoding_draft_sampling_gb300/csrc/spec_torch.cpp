@@ -11,10 +11,12 @@
 #include <ATen/core/Tensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <cuda_runtime_api.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstring>
@@ -268,19 +270,81 @@ PyObject* cache_read(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObjec
 // ---------------------------------------------------------------------------
 // attention
 // ---------------------------------------------------------------------------
-// cache_attend's workspaces, one per device and stream: their control words
-// start at zero and every call leaves them so.
-Tensor attend_workspace(size_t bytes, c10::Device device, void* stream) {
-    static auto* kept = new std::map<std::pair<int, void*>, Tensor>;    // outlives the interpreter's end
-    Tensor& ws = (*kept)[{device.index(), stream}];
-    if (!ws.defined() || static_cast<size_t>(ws.numel()) < bytes) {
-        if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None)
-            refuse("cache_attend needs its workspace before a stream capture: call it once before, or pass ws (zeroed)");
-        const c10::cuda::CUDAStreamGuard on(
-            c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream), device.index()));
-        ws = at::zeros({static_cast<int64_t>(bytes)}, at::TensorOptions(device).dtype(at::kByte));
+// cache_attend's workspaces: their control words start at zero and every call
+// leaves them so.  Calls on a stream share one, which is replaced when a call needs
+// more (its memory is freed in the stream's order).  A capture cannot have that one:
+// a graph keeps the address, and may be replayed beside other calls or graphs.  It
+// gets its own on each stream, zeroed by the graph, that lives until the graph and
+// all that was instantiated from it are gone.
+struct Held {
+    Tensor ws;
+    Held* next;
+};
+std::atomic<Held*> g_gone{nullptr};             // what the graphs that are gone held
+
+// (called by the CUDA runtime: no CUDA call is allowed here, and freeing may be one)
+void CUDART_CB graph_gone(void* p) {
+    Held* h = static_cast<Held*>(p);
+    h->next = g_gone.load(std::memory_order_relaxed);
+    while (!g_gone.compare_exchange_weak(h->next, h, std::memory_order_release, std::memory_order_relaxed)) {}
+}
+
+void free_gone() {
+    if (!g_gone.load(std::memory_order_relaxed)) return;
+    for (Held* h = g_gone.exchange(nullptr, std::memory_order_acquire); h;) {
+        Held* next = h->next;
+        delete h;
+        h = next;
     }
-    return ws;
+}
+
+void runtime(cudaError_t e, const char* what) {
+    if (e == cudaSuccess) return;
+    cudaGetLastError();
+    refuse("cache_attend: %s: %s", what, cudaGetErrorString(e));
+}
+
+Tensor attend_workspace(size_t bytes, c10::Device device, void* stream) {
+    struct Captured {
+        unsigned long long id;
+        Tensor ws;
+    };
+    using Key = std::pair<int, void*>;
+    static auto* eager = new std::map<Key, Tensor>;             // (both outlive the interpreter's end)
+    static auto* captured = new std::map<Key, Captured>;
+    const auto st = static_cast<cudaStream_t>(stream);
+    const Key key{device.index(), stream};
+    const auto is_enough = [&](const Tensor& t) { return t.defined() && static_cast<size_t>(t.numel()) >= bytes; };
+    free_gone();
+
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    unsigned long long id = 0;
+    cudaGraph_t graph = nullptr;
+    const cudaGraphNode_t* nodes = nullptr;
+    const cudaGraphEdgeData* edges = nullptr;
+    size_t count = 0;
+    runtime(cudaStreamGetCaptureInfo(st, &status, &id, &graph, &nodes, &edges, &count), "the stream's capture");
+    const bool capturing = status == cudaStreamCaptureStatusActive;
+    Captured* mine = capturing ? &(*captured)[key] : nullptr;
+    Tensor& kept = capturing ? mine->ws : (*eager)[key];
+    if (is_enough(kept) && (!capturing || mine->id == id)) return kept;
+
+    const c10::cuda::CUDAStreamGuard on(c10::cuda::getStreamFromExternal(st, device.index()));
+    const Tensor fresh = at::empty({static_cast<int64_t>(bytes)}, at::TensorOptions(device).dtype(at::kByte));
+    fresh.narrow(0, 0, SPEC_CACHE_WS_CONTROL).zero_();
+    if (capturing) {
+        auto* h = new Held{fresh, nullptr};
+        cudaUserObject_t object;
+        const cudaError_t made = cudaUserObjectCreate(&object, h, graph_gone, 1, cudaUserObjectNoDestructorSync);
+        if (made != cudaSuccess) delete h;
+        runtime(made, "the graph's workspace");
+        const cudaError_t kept_by = cudaGraphRetainUserObject(graph, object, 1, cudaGraphUserObjectMove);
+        if (kept_by != cudaSuccess) cudaUserObjectRelease(object, 1);
+        runtime(kept_by, "the graph's workspace");
+        mine->id = id;
+    }
+    kept = fresh;
+    return fresh;
 }
 
 PyObject* cache_attend(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kw) {
@@ -503,8 +567,9 @@ PyMethodDef g_methods[] = {
      "or without a mask the rows up to itself.  Its position is ctx_len[b] + depth[b, i]\n"
      "(default i); with window > 0 it sees only keys of position p with p_i - p < window or\n"
      "p < sinks.  scale defaults to 1/sqrt(D).  Rows that see nothing are 0, their lse -inf;\n"
-     "lse (natural log) is written when given or asked for.  A ws of one's own starts zeroed\n"
-     "and serves one stream."},
+     "lse (natural log) is written when given or asked for.  Without a ws, calls on a stream\n"
+     "share one and a captured graph has its own.  A ws of one's own starts zeroed, serves one\n"
+     "stream, and outlives the graphs that were captured with it."},
     {"cache_compact", fn(cache_compact), METH_FASTCALL | METH_KEYWORDS,
      "cache_compact(pool, page_table, ctx_len, path_nodes, num_accepted, head_dim, *, status=None, stream=None)\n\n"
      "Keep an accepted path's rows: position ctx_len[b] + path_nodes[b, j] moves to\n"
