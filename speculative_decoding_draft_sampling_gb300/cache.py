@@ -9,7 +9,9 @@ A block holds one page of P tokens of one kv head:
     K codes [P][D/2] | K scales bf16 [P][D/32] | V codes [P][D/2] | V scales bf16 [P][D/32]
 
 page_table [B, M] int32 names the pages of each request in order (-1: none).
-`status` arguments are optional int32 [B] tensors; bits are OR-ed in.
+`status` arguments are optional int32 [B] tensors; bits are OR-ed in.  A call
+runs on the current stream, or on the one given as `stream`, and what it
+allocates belongs to that stream, as under `torch.cuda.stream(stream)`.
 
   cache_append   quantise rows of K and V into the cache
   cache_read     rows of the cache as bf16 values

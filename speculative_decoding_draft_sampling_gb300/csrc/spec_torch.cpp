@@ -22,6 +22,7 @@
 #include <cstring>
 #include <initializer_list>
 #include <map>
+#include <optional>
 #include <string>
 #include <utility>
 
@@ -187,16 +188,28 @@ struct Table {
     }
 };
 
-// The stream that a call runs on: the one given, else the device's current one.
-void* stream_of(PyObject* o, c10::Device device) {
-    if (!o) return c10::cuda::getCurrentCUDAStream(device.index()).stream();
-    PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
-    if (!h) throw Raised{};
-    void* p = PyLong_AsVoidPtr(h);
-    Py_DECREF(h);
-    if (!p && PyErr_Occurred()) throw Raised{};
-    return p;
-}
+// The stream that a call runs on: the one given, else the device's current one.  It is
+// the current one while the call lasts, so that what the call allocates belongs to it.
+class Stream {
+    const c10::cuda::OptionalCUDAGuard device_;
+    std::optional<c10::cuda::CUDAStreamGuard> on_;
+    void* raw_;
+
+  public:
+    Stream(PyObject* o, c10::Device device) : device_(device) {
+        if (!o) {
+            raw_ = c10::cuda::getCurrentCUDAStream(device.index()).stream();
+            return;
+        }
+        PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
+        if (!h) throw Raised{};
+        raw_ = PyLong_AsVoidPtr(h);
+        Py_DECREF(h);
+        if (!raw_ && PyErr_Occurred()) throw Raised{};
+        on_.emplace(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(raw_), device.index()));
+    }
+    operator void*() const { return raw_; }
+};
 
 // A call's body, with C++ exceptions turned into Python's.
 template <class F>
@@ -229,11 +242,10 @@ PyObject* cache_append(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObj
         const int32_t* start = ints(a.v[4], "start", {B});
         const int32_t* count = ints_or_null(a.v[5], "count", {B});
         int32_t* status = ints_or_null(a.v[6], "status", {B});
-        const c10::cuda::OptionalCUDAGuard guard(pool.device);
+        const Stream stream(a.v[7], pool.device);
         done(g_api.append(k.data_ptr(), k.stride(0), k.stride(1), k.stride(2), v.data_ptr(), v.stride(0), v.stride(1),
                           v.stride(2), pool.data, pool.page_stride, pool.head_stride, pool.pages, t.data, t.stride,
-                          t.width, start, count, B, n, pool.heads, D, pool.page, status,
-                          stream_of(a.v[7], pool.device)),
+                          t.width, start, count, B, n, pool.heads, D, pool.page, status, stream),
              "spec_cache_append");
         Py_RETURN_NONE;
     });
@@ -251,7 +263,7 @@ PyObject* cache_read(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObjec
         const int32_t* start = ints(a.v[2], "start", {B});
         const int32_t* count = ints_or_null(a.v[5], "count", {B});
         int32_t* status = ints_or_null(a.v[8], "status", {B});
-        const c10::cuda::OptionalCUDAGuard guard(pool.device);
+        const Stream stream(a.v[9], pool.device);
         Tensor out[2];
         for (int i = 0; i < 2; ++i) {
             if (a.v[6 + i])
@@ -261,7 +273,7 @@ PyObject* cache_read(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObjec
         }
         done(g_api.read(pool.data, pool.page_stride, pool.head_stride, pool.pages, t.data, t.stride, t.width, start,
                         count, B, n, pool.heads, D, pool.page, out[0].data_ptr(), out[1].data_ptr(), status,
-                        stream_of(a.v[9], pool.device)),
+                        stream),
              "spec_cache_read");
         return Py_BuildValue("(NN)", THPVariable_Wrap(out[0]), THPVariable_Wrap(out[1]));
     });
@@ -304,6 +316,7 @@ void runtime(cudaError_t e, const char* what) {
     refuse("cache_attend: %s: %s", what, cudaGetErrorString(e));
 }
 
+// (the stream is the current one)
 Tensor attend_workspace(size_t bytes, c10::Device device, void* stream) {
     struct Captured {
         unsigned long long id;
@@ -329,7 +342,6 @@ Tensor attend_workspace(size_t bytes, c10::Device device, void* stream) {
     Tensor& kept = capturing ? mine->ws : (*eager)[key];
     if (is_enough(kept) && (!capturing || mine->id == id)) return kept;
 
-    const c10::cuda::CUDAStreamGuard on(c10::cuda::getStreamFromExternal(st, device.index()));
     const Tensor fresh = at::empty({static_cast<int64_t>(bytes)}, at::TensorOptions(device).dtype(at::kByte));
     fresh.narrow(0, 0, SPEC_CACHE_WS_CONTROL).zero_();
     if (capturing) {
@@ -370,14 +382,13 @@ PyObject* cache_attend(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObj
             scale = static_cast<float>(x);
         }
         int32_t* status = ints_or_null(a.v[13], "status", {B});
-        const c10::cuda::OptionalCUDAGuard guard(pool.device);
+        const Stream stream(a.v[15], pool.device);
         Tensor out = a.v[10] ? shaped(a.v[10], "out", at::kBFloat16, "bfloat16", {B, n, hq, D})
                              : at::empty({B, n, hq, D}, at::TensorOptions(pool.device).dtype(at::kBFloat16));
         Tensor lse;
         if (a.v[11]) lse = shaped(a.v[11], "lse", at::kFloat, "float32", {B, n, hq});
         else if (a.v[12] && PyObject_IsTrue(a.v[12]) > 0)
             lse = at::empty({B, n, hq}, at::TensorOptions(pool.device).dtype(at::kFloat));
-        void* stream = stream_of(a.v[15], pool.device);
         Tensor ws;
         if (a.v[14]) {
             ws = reachable(a.v[14], "ws", at::kByte, "uint8");
@@ -418,11 +429,11 @@ PyObject* cache_compact(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyOb
         const int32_t* ctx = ints(a.v[2], "ctx_len", {B});
         const int32_t* accepted = ints(a.v[4], "num_accepted", {B});
         int32_t* status = ints_or_null(a.v[6], "status", {B});
-        const c10::cuda::OptionalCUDAGuard guard(pool.device);
+        const Stream stream(a.v[7], pool.device);
         done(g_api.compact(pool.data, pool.layers, pool.layer_stride, pool.page_stride, pool.head_stride, pool.pages,
                            t.data, t.stride, t.width, ctx, static_cast<const int32_t*>(path.data_ptr()),
                            checked(path.size(1), "path_width"), accepted, B, pool.heads, D, pool.page, status,
-                           stream_of(a.v[7], pool.device)),
+                           stream),
              "spec_cache_compact");
         Py_RETURN_NONE;
     });
@@ -479,9 +490,9 @@ PyObject* grow_or_shrink(const char* who, decltype(&spec_cache_reserve) call, co
         const Pages s(a.v[0]);
         const int32_t* length = ints(a.v[1], "length", {s.R});
         int32_t* status = ints_or_null(a.v[3], "status", {s.R});
-        const c10::cuda::OptionalCUDAGuard guard(s.device);
+        const Stream stream(a.v[4], s.device);
         done(call(s.table->data, s.table->stride, s.table->width, s.held, s.ref, s.free_list, s.num_free, s.count,
-                  length, s.R, a.int32(2, 0, "page_size"), status, stream_of(a.v[4], s.device)),
+                  length, s.R, a.int32(2, 0, "page_size"), status, stream),
              c_name);
         Py_RETURN_NONE;
     });
@@ -507,13 +518,13 @@ PyObject* cache_fork(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObjec
         const int32_t* dst = ints(a.v[3], "dst", {F});
         const int32_t* length = ints(a.v[4], "length", {s.R});
         int32_t* status = ints_or_null(a.v[7], "status", {F});
-        const c10::cuda::OptionalCUDAGuard guard(pool.device);
+        const Stream stream(a.v[8], pool.device);
         const Tensor fresh = a.v[6] ? shaped(a.v[6], "new_page", at::kInt, "int32", {F})
                                     : at::empty({F}, at::TensorOptions(pool.device).dtype(at::kInt));
         done(g_api.fork(pool.data, pool.layers, pool.layer_stride, pool.page_stride, pool.head_stride, s.table->data,
                         s.table->stride, s.table->width, s.held, s.ref, s.free_list, s.num_free, s.count, src, dst,
                         length, s.R, F, pool.heads, D, pool.page, static_cast<int32_t*>(fresh.data_ptr()), status,
-                        stream_of(a.v[8], pool.device)),
+                        stream),
              "spec_cache_fork");
         return THPVariable_Wrap(fresh);
     });

@@ -115,3 +115,48 @@ def test_workspaces_of_dropped_graphs_are_freed(cache):
         at[i] = torch.cuda.memory_allocated()
     size = sv.cache._lib().spec_cache_attend_workspace_size(len(CTX), 40, 4 * H, H, D)
     assert at[24] - at[4] < 5 * size, (at, size)
+
+
+def stream_of(t):
+    """The stream whose memory a tensor lies in."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+
+
+def test_what_a_call_allocates_belongs_to_its_stream(cache):
+    pool, table, ctx = cache
+    side = torch.cuda.Stream()
+    q, pages = randn(len(CTX), 2, 4 * H, D), sv.page_state(2, 4, pool.shape[0], DEV)
+    sv.cache_reserve(pages, ints([70, 0]), P)
+    own = torch.zeros_like(pool)[None]                   # (fork writes into it)
+    args = [ints([0] * len(CTX)), ints([0]), ints([1]), ints([70, 0])]
+    torch.cuda.synchronize()
+    k, v = sv.cache_read(pool, table, args[0], 200, D, stream=side)
+    a = sv.cache_attend(q, pool, table, ctx, want_lse=True, stream=side)
+    new = sv.cache_fork(own, pages, *args[1:], D, stream=side)
+    side.synchronize()
+    for t in (k, v, a.out, a.lse, a.ws, new):
+        assert stream_of(t) == side.cuda_stream
+    assert torch.equal(a.out, sv.cache_attend(q, pool, table, ctx).out)
+
+
+def test_given_stream_of_a_capture(cache):
+    """A stream that joined the capture is given; the current stream's calls are captured too."""
+    pool, table, ctx = cache
+    q = randn(len(CTX), 2, 4 * H, D)
+    want = sv.cache_attend(q, pool, table, ctx).out.clone()
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        a = sv.cache_attend(q, pool, table, ctx, stream=side)
+        b = sv.cache_attend(q, pool, table, ctx)
+        torch.cuda.current_stream().wait_stream(side)
+    assert a.ws.data_ptr() != b.ws.data_ptr()
+    for _ in range(3):
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a.out, want) and torch.equal(b.out, want)
+        a.out.zero_()
+        b.out.zero_()
