@@ -42,6 +42,7 @@ extern "C" {
 
 #define SPEC_ST_BAD_PAGE 128   /* a needed position has no page (or a page id / request id out of range) */
 #define SPEC_ST_NO_PAGE  256   /* the free pages did not suffice: the request got none */
+#define SPEC_ST_SHARED_PAGE 512 /* a request ends inside a page that others hold too: rows must not be written there */
 
 /* bytes at the start of spec_cache_attend's workspace that begin zeroed */
 #define SPEC_CACHE_WS_CONTROL 16384
@@ -157,6 +158,13 @@ spec_status spec_cache_compact(
  * spec_cache_release: request r keeps the pages of length[r] tokens (0 frees
  *   the request); the others lose a reference, and those that nothing holds
  *   any more are pushed on the stack in ascending order.
+ *   A page that a fork made shared is for reading: spec_cache_append and
+ *   spec_cache_compact write where they are told to and would change the other
+ *   holders' rows.  A request only comes to write there when it is cut back to
+ *   a length inside a shared page; release says so (SPEC_ST_SHARED_PAGE, after
+ *   all of the call's references are dropped).  To go on from such a length,
+ *   fork the request at it, which gives the copy a page of its own for the
+ *   rest, and release the request itself.
  * spec_cache_fork: request dst[f] becomes a copy of request src[f] at
  *   length[src[f]] tokens: it shares the full pages and gets one of its own
  *   for the rest, taken as in reserve, into which the rest's rows are copied

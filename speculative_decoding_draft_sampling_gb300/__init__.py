@@ -597,7 +597,8 @@ def adaptive_len(conf, a: float, b: float, *, cost=None, out: Optional[AdaptiveL
 # the paged 4-bit cache
 # ---------------------------------------------------------------------------
 from . import cache  # noqa: E402
-from .cache import ST_BAD_PAGE, ST_NO_PAGE, CacheAttention, PageState, cache_block_bytes, page_state  # noqa: E402
+from .cache import (ST_BAD_PAGE, ST_NO_PAGE, ST_SHARED_PAGE, CacheAttention, PageState,  # noqa: E402
+                    cache_block_bytes, page_state)
 
 
 def __getattr__(name: str):

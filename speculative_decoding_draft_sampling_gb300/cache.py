@@ -34,7 +34,7 @@ import torch
 
 from . import LIB_PATH, SpecError, _load
 
-ST_BAD_PAGE, ST_NO_PAGE = 128, 256
+ST_BAD_PAGE, ST_NO_PAGE, ST_SHARED_PAGE = 128, 256, 512
 
 BINDING_PATH = os.path.join(os.path.dirname(LIB_PATH), "_spec_torch.so")
 

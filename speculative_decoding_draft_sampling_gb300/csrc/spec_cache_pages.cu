@@ -170,6 +170,17 @@ __global__ void __launch_bounds__(kPageThreads) cache_release_kernel(const Cache
         }
         __syncthreads();
     }
+    // Requests that were cut back into a page which others hold as well: whoever writes
+    // there writes the others' rows.  Looked for only where somebody asks; all
+    // references are dropped by now.
+    if (A.status)
+        for (int r = threadIdx.x; r < A.R; r += kPageThreads) {
+            const int length = A.length[r], last = pages_for(length, A.p_shift) - 1;
+            if (length <= 0 || !(length & ((1 << A.p_shift) - 1)) || last >= clamp_held(A.held[r], A.width)) continue;
+            const int page = A.table[r * A.stride + last];
+            if (static_cast<unsigned>(page) < static_cast<unsigned>(A.num_pages) && __ldcg(A.ref + page) > 1)
+                atomicOr(A.status + r, SPEC_ST_SHARED_PAGE);
+        }
     int top = stack_size(A);
     for (int i0 = 0; i0 < words; i0 += kPageThreads) {
         const int i = i0 + static_cast<int>(threadIdx.x);

@@ -593,7 +593,8 @@ PyMethodDef g_methods[] = {
     {"cache_release", fn(cache_release), METH_FASTCALL | METH_KEYWORDS,
      "cache_release(pages, length, page_size, *, status=None, stream=None)\n\n"
      "Each request keeps the pages of length[r] tokens (0: none); pages that nothing holds any\n"
-     "more are free."},
+     "more are free.  A request cut back to a length inside a page that a fork made shared must\n"
+     "not be written to (ST_SHARED_PAGE): fork it at that length and release it instead."},
     {"cache_fork", fn(cache_fork), METH_FASTCALL | METH_KEYWORDS,
      "cache_fork(pool, pages, src, dst, length, head_dim, *, new_page=None, status=None, stream=None)\n\n"
      "Request dst[f] (holding nothing) becomes a copy of request src[f] at length[src[f]]\n"
