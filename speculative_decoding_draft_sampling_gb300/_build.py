@@ -17,6 +17,7 @@ LIBDIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIBDIR, "libspecverify.so")
 BINDING = os.path.join(LIBDIR, "_spec_torch.so")
 BINDING_SRC = os.path.join(CSRC, "spec_torch.cpp")
+BINDING_FOR = os.path.join(LIBDIR, "_spec_torch.for")      # what the binding was built against
 ROOT = os.path.dirname(HERE)
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -46,9 +47,18 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def _built_for() -> str:
+    """The binding uses PyTorch's and Python's C++ interfaces, which hold for one version."""
+    import torch
+    return f"torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}"
+
+
 def binding_up_to_date() -> bool:
-    if not os.path.exists(BINDING):
+    if not os.path.exists(BINDING) or not os.path.exists(BINDING_FOR):
         return False
+    with open(BINDING_FOR) as f:
+        if f.read() != _built_for():
+            return False
     t = os.path.getmtime(BINDING)
     return all(os.path.getmtime(p) <= t for p in [BINDING_SRC] + glob.glob(os.path.join(ROOT, "include", "*.h")))
 
@@ -69,6 +79,8 @@ def build_binding() -> str:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    with open(BINDING_FOR, "w") as f:
+        f.write(_built_for())
     return BINDING
 
 
