@@ -123,6 +123,8 @@ struct CacheAttendArgs {
     void* ws;
 };
 size_t cache_attend_ws(int B, int n, int hq, int hkv, int D);
+// tiles that a request of this many positions may come to, over all kv heads and blocks of rows
+long long cache_attend_tiles(int n, int hq, int hkv, long long positions);
 cudaError_t cache_attend_run(const CacheAttendArgs& A, cudaStream_t st);
 
 }  // namespace spec

@@ -166,10 +166,15 @@ spec_status spec_cache_attend(
     if (B > 65535 || q_heads > 65535) return fail(SPEC_UNSUPPORTED, "%s: at most 65535 requests and q heads", who);
     if (B == 0 || n == 0) return SPEC_OK;
     spec::CacheAttendArgs A{};
-    CACHE_TRY(pool_of(who, pool, 1, 0, page_stride, head_stride, num_pages, kv_heads, head_dim, page_size, A.pool));
-    CACHE_TRY(table_of(who, page_table, table_stride, table_width, A.tab));
+    // positions, and a request's tiles over all kv heads and blocks of rows, are counted in 32 bits
     if (static_cast<long long>(table_width) * page_size > 0x7fff0000LL)
         return fail(SPEC_UNSUPPORTED, "%s: a table of more than 2^31 positions", who);
+    if (table_width > 0 && shift_of(page_size) >= 0 &&
+        spec::cache_attend_tiles(n, q_heads, kv_heads, static_cast<long long>(table_width) * page_size) > 0x7fffffffLL)
+        return fail(SPEC_UNSUPPORTED, "%s: %d pages of %d tokens a request are too many for %d rows of %d q heads", who,
+                    table_width, page_size, n, q_heads);
+    CACHE_TRY(pool_of(who, pool, 1, 0, page_stride, head_stride, num_pages, kv_heads, head_dim, page_size, A.pool));
+    CACHE_TRY(table_of(who, page_table, table_stride, table_width, A.tab));
     if (!q || !ctx_len || !out) return fail(SPEC_INVALID_ARG, "%s: null pointer argument", who);
     if (reinterpret_cast<uintptr_t>(q) % 2 || reinterpret_cast<uintptr_t>(out) % 16)
         return fail(SPEC_INVALID_ARG, "%s: q must be 2-byte and out 16-byte aligned", who);

@@ -692,9 +692,6 @@ cudaError_t attend(const CacheAttendArgs& A, cudaStream_t st) {
     L.grid = grid;
     L.row_tiles = (A.n * A.G + Cfg::kRows - 1) / Cfg::kRows;
     L.min_tiles = 1;
-    // a request's tiles are counted in 32 bits
-    const long long tiles = ((static_cast<long long>(A.tab.width) << A.pool.p_shift) + A.n) / kTile + 2;
-    if (tiles * A.pool.heads * L.row_tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
     unsigned char* ws = static_cast<unsigned char*>(A.ws);
     L.ctrl = reinterpret_cast<AttendCtrl*>(ws);
     L.ml = reinterpret_cast<float*>(ws + y.ml);
@@ -735,6 +732,13 @@ size_t cache_attend_ws(int B, int n, int hq, int hkv, int D) {
     if (R > kFewRows) return attend_tc_ws(D);
     const int NT = row_blocks(R);
     return AttendLayout(2 * min(attend_sms() * ctas_of(NT), kMaxGrid), 8 * NT, D).bytes;
+}
+
+long long cache_attend_tiles(int n, int hq, int hkv, long long positions) {
+    const int R = n * (hq / hkv);
+    if (R > kFewRows) return attend_tc_tiles(R, hkv, positions + n);
+    const int rows = 8 * row_blocks(R);
+    return ((positions + n) / kTile + 2) * hkv * ((R + rows - 1) / rows);
 }
 
 cudaError_t cache_attend_run(const CacheAttendArgs& A, cudaStream_t st) {

@@ -383,6 +383,7 @@ struct AttendLayout {
 
 // many rows a kv head: tcgen05 (spec_cache_attend_tc.cu)
 size_t attend_tc_ws(int D);
+long long attend_tc_tiles(int R, int hkv, long long positions);
 cudaError_t attend_tc_run(const CacheAttendArgs& A, cudaStream_t st);
 
 }  // namespace spec

@@ -819,8 +819,6 @@ cudaError_t attend_tc(const CacheAttendArgs& A, cudaStream_t st) {
     L.grid = grid;
     L.row_tiles = (A.n * A.G + kRows - 1) / kRows;
     L.min_tiles = 2;
-    const long long tiles = ((static_cast<long long>(A.tab.width) << A.pool.p_shift) + A.n) / kTok + 2;
-    if (tiles * A.pool.heads * L.row_tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
     unsigned char* ws = static_cast<unsigned char*>(A.ws);
     L.ctrl = reinterpret_cast<AttendCtrl*>(ws);
     L.ml = reinterpret_cast<float*>(ws + y.ml);
@@ -843,6 +841,10 @@ extern "C" int spec_test_drop_commit(int on) { return static_cast<int>(cudaMemcp
 #endif
 
 size_t attend_tc_ws(int D) { return AttendLayout(2 * min(attend_sms(), kMaxGrid / 2), kRows, D).bytes; }
+
+long long attend_tc_tiles(int R, int hkv, long long positions) {
+    return (positions / kTok + 2) * hkv * ((R + kRows - 1) / kRows);
+}
 
 cudaError_t attend_tc_run(const CacheAttendArgs& A, cudaStream_t st) {
     return A.pool.D == 128 ? attend_tc<128>(A, st) : attend_tc<64>(A, st);
