@@ -100,7 +100,7 @@ spec_status spec_cache_read(
  *   anc_mask NULL or [B, n, ceil(n/64)] uint64, as spec_tree_build writes it;
  *            depth NULL or [B, n] int32, cut to [0, n] (both, or a mask
  *            alone: depth = i).
- *   scale    multiplies q . k (> 0, finite).
+ *   scale    multiplies q . k (> 0, < 1.4e37).
  * Outputs: out bf16 [B, n, q_heads, D] contiguous: softmax over the seen keys
  *   times V; lse NULL or fp32 [B, n, q_heads]: natural log of the softmax's
  *   denominator.  Rows that see nothing, and rows i >= num_rows[b], are 0 with

@@ -1,7 +1,5 @@
 // spec_cache_api.cu -- the C ABI of the paged 4-bit cache: argument checks and
 // launches.  Nothing here allocates, synchronises or throws.
-#include <cmath>
-
 #include "../../include/spec_cache.h"
 #include "spec_cache.cuh"
 #include "spec_host.cuh"
@@ -160,7 +158,8 @@ spec_status spec_cache_attend(
         return fail(SPEC_INVALID_ARG, "%s: q_heads must be a multiple of kv_heads (got %d and %d)", who, q_heads,
                     kv_heads);
     if (window < 0 || sinks < 0) return fail(SPEC_INVALID_ARG, "%s: need window >= 0 and sinks >= 0", who);
-    if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(SPEC_INVALID_ARG, "%s: need a finite scale > 0", who);
+    // the kernels multiply by 16 scale log2 e
+    if (!(scale > 0.0f) || !(scale < 1.4e37f)) return fail(SPEC_INVALID_ARG, "%s: need a scale > 0 and < 1.4e37", who);
     if (depth && !anc_mask) return fail(SPEC_INVALID_ARG, "%s: depth goes with anc_mask", who);
     if (n > 1024) return fail(SPEC_UNSUPPORTED, "%s: at most 1024 rows a request (got %d)", who, n);
     if (B > 65535 || q_heads > 65535) return fail(SPEC_UNSUPPORTED, "%s: at most 65535 requests and q heads", who);

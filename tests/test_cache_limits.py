@@ -1,7 +1,7 @@
 """What the attention over the cache refuses for its size, before any device work."""
 import pytest
 
-from test_cache_abi import UNSUPPORTED, _attend, _err, lib  # noqa: F401
+from test_cache_abi import INVALID, UNSUPPORTED, _attend, _err, lib  # noqa: F401
 
 
 @pytest.mark.parametrize("kw,text", [
@@ -12,3 +12,10 @@ from test_cache_abi import UNSUPPORTED, _attend, _err, lib  # noqa: F401
 def test_attend_refuses_tables_that_are_too_large(lib, kw, text):                       # noqa: F811
     assert _attend(lib, **kw) == UNSUPPORTED
     assert text in _err(lib)
+
+
+@pytest.mark.parametrize("scale", [1.5e37, 3e38])
+def test_attend_refuses_scales_that_overflow(lib, scale):                               # noqa: F811
+    """16 scale log2 e has to be finite."""
+    assert _attend(lib, scale=scale) == INVALID
+    assert "scale > 0 and < 1.4e37" in _err(lib)
