@@ -605,6 +605,5 @@ def __getattr__(name: str):
     """The cache calls are the binding's own functions, put in place at the
     first use of one (importing the package loads no library)."""
     if name in cache.CALLS:
-        cache.bind((globals(), cache.__dict__))
-        return globals()[name]
+        return getattr(cache, name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

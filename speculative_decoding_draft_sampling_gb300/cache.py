@@ -27,6 +27,7 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import os
+import sys
 from dataclasses import dataclass
 from typing import Optional
 
@@ -121,8 +122,11 @@ def cache_block_bytes(head_dim: int, page_size: int) -> int:
 CALLS = ("cache_append", "cache_read", "cache_attend", "cache_compact", "cache_reserve", "cache_release", "cache_fork")
 
 
-def bind(namespaces) -> None:
-    """Put the binding's functions into the given namespaces."""
-    module = _binding()
-    for space in namespaces:
-        space.update({name: getattr(module, name) for name in CALLS})
+def __getattr__(name: str):
+    """The first use of a call puts the binding's functions here and into the package."""
+    if name in CALLS:
+        module = _binding()
+        for space in (globals(), vars(sys.modules[__package__])):
+            space.update({call: getattr(module, call) for call in CALLS})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
