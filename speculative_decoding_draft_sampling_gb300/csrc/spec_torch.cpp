@@ -64,12 +64,23 @@ void done(spec_status rc, const char* who) {
     if (rc != SPEC_OK) refuse("%s failed (status %d): %s", who, static_cast<int>(rc), g_api.last_error());
 }
 
+// CUDA tensors lie where the call works (host tensors are checked for being pinned).
+void on_device(PyObject* o, const char* name, c10::Device device) {
+    if (!o || !THPVariable_Check(o)) return;
+    const Tensor& t = THPVariable_Unpack(o);
+    if (t.is_cuda() && t.device() != device)
+        refuse("%s is on %s, the call works on %s", name, t.device().str().c_str(), device.str().c_str());
+}
+
 // Arguments of a call: positional ones, then keywords, in the order of `names`.
 struct Args {
     PyObject* v[16] = {};
+    const char* const* const names;
+    const int count;
 
-    Args(const char* who, const char* const* names, int count, int required, int positional, PyObject* const* args,
-         Py_ssize_t nargs, PyObject* kwnames) {
+    Args(const char* who, const char* const* names_, int count_, int required, int positional, PyObject* const* args,
+         Py_ssize_t nargs, PyObject* kwnames)
+        : names(names_), count(count_) {
         if (nargs > positional) {
             PyErr_Format(PyExc_TypeError, "%s() takes at most %d positional arguments (%zd given)", who, positional, nargs);
             throw Raised{};
@@ -95,6 +106,9 @@ struct Args {
                 throw Raised{};
             }
         }
+    }
+    void all_on(c10::Device device) const {
+        for (int i = 0; i < count; ++i) on_device(v[i], names[i], device);
     }
     long long integer(int i, long long fallback) const {
         if (!v[i]) return fallback;
@@ -236,6 +250,7 @@ PyObject* cache_append(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObj
             refuse("k and v must be [B, n, kv_heads, D] with unit element stride");
         const int B = checked(k.size(0), "B"), n = checked(k.size(1), "n"), D = checked(k.size(3), "D");
         const Pool pool(a.v[2], 3, D);
+        a.all_on(pool.device);
         if (pool.heads != k.size(2))
             refuse("the pool has %d kv heads, k and v %lld", pool.heads, static_cast<long long>(k.size(2)));
         const Table t(a.v[3], B);
@@ -257,6 +272,7 @@ PyObject* cache_read(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObjec
         const Args a("cache_read", names, 10, 5, 6, args, nargs, kw);
         const int n = a.int32(3, 0, "n"), D = a.int32(4, 0, "head_dim");
         const Pool pool(a.v[0], 3, D);
+        a.all_on(pool.device);
         const Table t(a.v[1], -1);
         const int B = checked(t.rows, "B");
         if (n < 0) refuse("n must not be negative");
@@ -369,6 +385,7 @@ PyObject* cache_attend(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObj
         const int B = checked(q.size(0), "B"), n = checked(q.size(1), "n"), hq = checked(q.size(2), "q_heads"),
                   D = checked(q.size(3), "D");
         const Pool pool(a.v[1], 3, D);
+        a.all_on(pool.device);
         const Table t(a.v[2], B);
         const int32_t* ctx = ints(a.v[3], "ctx_len", {B});
         const int32_t* rows = ints_or_null(a.v[4], "num_rows", {B});
@@ -421,6 +438,7 @@ PyObject* cache_compact(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyOb
         const Args a("cache_compact", names, 8, 6, 6, args, nargs, kw);
         const int D = a.int32(5, 0, "head_dim");
         const Pool pool(a.v[0], 4, D);
+        a.all_on(pool.device);
         const Table t(a.v[1], -1);
         const int B = checked(t.rows, "B");
         const Tensor& path = reachable(a.v[3], "path_nodes", at::kInt, "int32");
@@ -456,17 +474,18 @@ struct Pages {
                 owned[i] = PyObject_GetAttr(o, interned[i]);
                 if (!owned[i]) throw Raised{};
             }
+            const Tensor& r = reachable(owned[2], "ref", at::kInt, "int32");
+            if (!r.is_cuda()) refuse("ref must be device memory");
+            device = r.device();
+            for (int i = 0; i < 5; ++i) on_device(owned[i], names[i], device);
             table = new Table(owned[0], -1);
             R = checked(table->rows, "requests");
-            const Tensor& r = reachable(owned[2], "ref", at::kInt, "int32");
             const int64_t n = r.dim() == 1 ? r.size(0) : -1;
             ref = ints(owned[2], "ref", {n});
             held = ints(owned[1], "num_held", {R});
             free_list = ints(owned[3], "free_list", {n});
             num_free = ints(owned[4], "num_free", {1});
             count = checked(n, "pages");
-            if (!r.is_cuda()) refuse("ref must be device memory");
-            device = r.device();
         } catch (...) {
             release();
             throw;
@@ -488,6 +507,7 @@ PyObject* grow_or_shrink(const char* who, decltype(&spec_cache_reserve) call, co
         static const char* const names[] = {"pages", "length", "page_size", "status", "stream"};
         const Args a(who, names, 5, 3, 3, args, nargs, kw);
         const Pages s(a.v[0]);
+        a.all_on(s.device);
         const int32_t* length = ints(a.v[1], "length", {s.R});
         int32_t* status = ints_or_null(a.v[3], "status", {s.R});
         const Stream stream(a.v[4], s.device);
@@ -510,7 +530,10 @@ PyObject* cache_fork(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObjec
         const Args a("cache_fork", names, 9, 6, 6, args, nargs, kw);
         const int D = a.int32(5, 0, "head_dim");
         const Pool pool(a.v[0], 4, D);
+        a.all_on(pool.device);
         const Pages s(a.v[1]);
+        if (s.device != pool.device)
+            refuse("the state is on %s, the pool on %s", s.device.str().c_str(), pool.device.str().c_str());
         if (s.count != pool.pages) refuse("the state has %d pages, the pool %d", s.count, pool.pages);
         const Tensor& first = reachable(a.v[2], "src", at::kInt, "int32");
         const int F = checked(first.dim() == 1 ? first.size(0) : -1, "forks");
