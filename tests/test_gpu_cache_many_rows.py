@@ -105,10 +105,31 @@ def test_scores_that_rise_and_fall(D, B, H, n, G):
 
 
 @both
-@few
-def test_large_scores(D, P, n, hq, H):
-    ctx = [150, 1700]
-    attend(*case(ctx, n, hq, H, D, P, seed=2), ctx, scale=40.0)
+@shapes
+def test_large_scores_pick_one_key(D, P, n, hq, H):
+    """Scores of several thousands.  Where one key leads by more than 100 (e^-100 is 0 even beside a maximum that
+    has yet to move by 2^8) the output is its value, exactly, and lse its score."""
+    ctx, G = [150, 1700], hq // H
+    q, pool, table = case(ctx, n, hq, H, D, P, seed=2)
+    r = sv.cache_attend(q, pool, table, ints(ctx), want_lse=True, scale=40.0)
+    out, lse = r.out.double().cpu().numpy(), r.lse.double().cpu().numpy()
+    ref = cache_ref.Pool(pool, D)
+    keys, vals = cache_ref.values(ref, "k"), cache_ref.values(ref, "v")
+    led = 0
+    for b, c in enumerate(ctx):
+        t = np.arange(c + n)
+        page, slot = table[b].cpu().numpy()[t // P], t % P
+        see = cache_ref.seen_rows(c, n, n, None, None, 0, 0)
+        for h in range(hq):
+            k, v, y = keys[page, h // G, slot], vals[page, h // G, slot], q[b, :, h].double().cpu().numpy()
+            x = np.where(see, 40.0 * (y @ k.T), -np.inf)
+            order = np.sort(x, -1)
+            lead = order[:, -1] - order[:, -2] > 100
+            led += lead.sum()
+            assert (out[b, lead, h] == v[x.argmax(-1)][lead]).all()
+            size = 40.0 * (np.abs(y) @ np.abs(k).T).max(-1)
+            assert (np.abs(lse[b, lead, h] - order[lead, -1]) <= 2.0 ** -17 * (1 + 2 * size[lead])).all()
+    assert led > n * hq
 
 
 @few
