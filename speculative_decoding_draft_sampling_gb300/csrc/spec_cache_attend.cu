@@ -689,7 +689,6 @@ cudaError_t attend(const CacheAttendArgs& A, cudaStream_t st) {
     const AttendLayout y(2 * grid, Cfg::kRows, D);
     AttendPlan L;
     L.one2 = 0x3F803F80u;
-    L.grid = grid;
     L.row_tiles = (A.n * A.G + Cfg::kRows - 1) / Cfg::kRows;
     L.min_tiles = 1;
     unsigned char* ws = static_cast<unsigned char*>(A.ws);

@@ -46,7 +46,6 @@ constexpr int kMaxGrid = (SPEC_CACHE_WS_CONTROL - 256) / 4;
 
 struct AttendPlan {
     uint32_t one2;                              // 0x3F803F80 (codes2)
-    int grid;                                   // CTAs
     int row_tiles;                              // blocks of rows a (request, kv head)
     int min_tiles;                              // tiles worth a CTA
     float* ml;                                  // [2 * grid][rows of a block][4]: m, l, l of the rounded weights

@@ -816,7 +816,6 @@ cudaError_t attend_tc(const CacheAttendArgs& A, cudaStream_t st) {
     const AttendLayout y(2 * grid, kRows, D);
     AttendPlan L;
     L.one2 = 0x3F803F80u;
-    L.grid = grid;
     L.row_tiles = (A.n * A.G + kRows - 1) / kRows;
     L.min_tiles = 2;
     unsigned char* ws = static_cast<unsigned char*>(A.ws);

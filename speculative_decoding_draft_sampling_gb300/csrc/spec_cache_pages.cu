@@ -275,35 +275,34 @@ __global__ void __launch_bounds__(kCopyThreads) cache_copy_kernel(const CachePag
     const int codes = rows * Blk::kRow / 16, half = codes + rows;
     const int pairs = A.pool.layers * A.pool.heads;
     const long long move = (static_cast<long long>(to) - from) * A.pool.page_stride;
-    for (int p0 = blockIdx.x * kBlocks; p0 < pairs; p0 += gridDim.x * kBlocks) {
-        unsigned char* blk[kBlocks];
+    const int p0 = blockIdx.x * kBlocks;
+    unsigned char* blk[kBlocks];
 #pragma unroll
-        for (int q = 0; q < kBlocks; ++q) {
-            const int layer = (p0 + q) / A.pool.heads, head = (p0 + q) % A.pool.heads;
-            blk[q] = A.pool.base + layer * A.pool.layer_stride + head * A.pool.head_stride + from * A.pool.page_stride;
-        }
-        for (int w = threadIdx.x; w < 2 * half; w += kCopyThreads) {
-            const int x = w >= half ? w - half : w;
-            int at = w >= half ? Blk::v_codes(P) : 0;
-            if (x < codes) {
-                at += x * 16;
-                uint4 r[kBlocks];
+    for (int q = 0; q < kBlocks; ++q) {
+        const int layer = (p0 + q) / A.pool.heads, head = (p0 + q) % A.pool.heads;
+        blk[q] = A.pool.base + layer * A.pool.layer_stride + head * A.pool.head_stride + from * A.pool.page_stride;
+    }
+    for (int w = threadIdx.x; w < 2 * half; w += kCopyThreads) {
+        const int x = w >= half ? w - half : w;
+        int at = w >= half ? Blk::v_codes(P) : 0;
+        if (x < codes) {
+            at += x * 16;
+            uint4 r[kBlocks];
 #pragma unroll
-                for (int q = 0; q < kBlocks; ++q)
-                    if (p0 + q < pairs) r[q] = __ldcs(reinterpret_cast<const uint4*>(blk[q] + at));
+            for (int q = 0; q < kBlocks; ++q)
+                if (p0 + q < pairs) r[q] = __ldcs(reinterpret_cast<const uint4*>(blk[q] + at));
 #pragma unroll
-                for (int q = 0; q < kBlocks; ++q)
-                    if (p0 + q < pairs) *reinterpret_cast<uint4*>(blk[q] + at + move) = r[q];
-            } else {
-                at += P * Blk::kRow + (x - codes) * Blk::kScl;
-                Scl r[kBlocks];
+            for (int q = 0; q < kBlocks; ++q)
+                if (p0 + q < pairs) *reinterpret_cast<uint4*>(blk[q] + at + move) = r[q];
+        } else {
+            at += P * Blk::kRow + (x - codes) * Blk::kScl;
+            Scl r[kBlocks];
 #pragma unroll
-                for (int q = 0; q < kBlocks; ++q)
-                    if (p0 + q < pairs) r[q] = *reinterpret_cast<const Scl*>(blk[q] + at);
+            for (int q = 0; q < kBlocks; ++q)
+                if (p0 + q < pairs) r[q] = *reinterpret_cast<const Scl*>(blk[q] + at);
 #pragma unroll
-                for (int q = 0; q < kBlocks; ++q)
-                    if (p0 + q < pairs) *reinterpret_cast<Scl*>(blk[q] + at + move) = r[q];
-            }
+            for (int q = 0; q < kBlocks; ++q)
+                if (p0 + q < pairs) *reinterpret_cast<Scl*>(blk[q] + at + move) = r[q];
         }
     }
 }
