@@ -31,7 +31,8 @@ struct CacheBlock {
 // be set up while the kernel before it in the stream ends; every thread waits for that
 // end, and for all that was written, before it reads anything (and reads nothing as
 // constant: it may have been written after the launch).  A call takes 2 us less: one
-// request's attention 12.4 to 10.0, a batch's reserve, forks and release 93 to 86.
+// request's attention 12.4 to 10.0, a batch's reserve, forks and release 93 to 86 when it
+// was made.
 #ifdef __CUDACC__
 __device__ __forceinline__ void after_earlier() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // lets the next kernel's blocks be set up now

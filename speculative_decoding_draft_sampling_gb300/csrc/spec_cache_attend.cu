@@ -23,12 +23,16 @@
 // many CTAs an SM, and one barrier a tile is all they wait for each other.  (Tiles of
 // 128 tokens halve the barriers, but their registers cost a CTA an SM: slower.)
 //
-// What bounds it.  Up to 8 rows: turning codes into bf16, near half of a tile's
-// instructions (4 requests of 131072 tokens, 8 heads of 128, 4 rows a head: 124 us,
-// 3.5 TB/s of cache, 69 % of the issue slots).  From 16 rows on the tensor
-// instruction itself: a scheduler takes one in 8 cycles, 16 for every 8 rows of a tile
-// and warp (256 requests of 4096 tokens, 36 rows a head: 445 us, 218 TFLOP/s, those
-// cycles are 68 % of all).
+// What bounds it.  No unit is at its limit: a tile is a chain (codes, S^T, exponentials,
+// a barrier, O^T), and the three to six CTAs that an SM has registers for overlap
+// theirs.  All with 8 heads of 128 and lengths evenly from the first down to the second:
+//   4 rows a head, 4 requests of 131072 to 57344 tokens: 124 us, 434 MB, 3.5 TB/s.  68 %
+//       of the issue slots; 480 instructions a tile and warp, 192 turn codes into bf16.
+//   16 rows, 64 requests of 2048 to 536: 50 us.  54 % of the slots, 680 instructions a
+//       tile and warp; the tensor instruction (one in 8 cycles a scheduler, 16 for every 8
+//       rows of a tile and warp) 21 % of the time.  A CTA has only 14 tiles.
+//   36 rows, 256 requests of 4096 to 1036: 448 us, 217 TFLOP/s.  52 % of the slots, the
+//       tensor instruction 43 %; three CTAs an SM.
 // One request of a few hundred tokens takes 10 us: launch, the deal of the work, one
 // tile, the join.
 #include <atomic>
@@ -43,10 +47,10 @@ namespace {
 constexpr int kAtWarps = 4;
 constexpr int kAtThreads = 32 * kAtWarps;
 constexpr int kTile = 64;                       // tokens a tile
-// Rows a kv head that this kernel takes.  Its time grows with every 8 rows, the
-// tcgen05 kernel's hardly up to 128: 64 requests of 2048 tokens 76 / 106 / 142 / 234 us
-// at 32 / 48 / 64 / 96 rows against 150 / 160 / 150 / 154; 32 of 8192 193 against
-// 184 us at 64.
+// Rows a kv head that this kernel takes.  Its time grows with every 8 rows (past 48 it
+// would need two blocks of them), the tcgen05 kernel's hardly up to 128: 64 requests of
+// 2048 to 536 tokens 70 / 96 / 162 / 171 us at 32 / 48 / 64 / 96 rows against 110 / 111 /
+// 112 / 116; 32 of 8192 to 2240 246 against 145 us at 64.
 constexpr int kFewRows = 48;
 
 __device__ __forceinline__ uint32_t lds16(uint32_t a) {

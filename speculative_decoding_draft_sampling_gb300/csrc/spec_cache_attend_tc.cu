@@ -22,9 +22,10 @@
 //                rows is group 0's alone; its tiles take the two S in turn.
 // What bounds it, a tile of 128 tokens and 256 rows at D = 128: shared memory, 64 KB
 // written and 192 KB read by the tensor core at 128 bytes a cycle, and the tensor core
-// itself are busy 2048 cycles each; a tile takes 3700, because a group's products and
-// its exponentials follow one another (32 requests of 8192 tokens, 64-node trees of 4
-// heads a kv head: 220 us, 605 TFLOP/s).  What shortens one of the two but adds code or
+// itself are busy 2048 cycles each; a tile takes 5400, because a group's products and
+// its exponentials follow one another (32 requests of 8192 down to 2240 tokens, trees of
+// 64 down to 33 nodes, 4 heads a kv head: 212 to 221 us, 600 to 628 TFLOP/s; rows that are
+// not there are multiplied too).  What shortens one of the two but adds code or
 // registers lost: scores read once with a late rescale 237 us, a second tile of codes
 // in flight in registers 229, or in shared memory 226.  With up to 128 rows both groups
 // could take the tiles in turn: 183 us against 154 at 128 rows, for the join of

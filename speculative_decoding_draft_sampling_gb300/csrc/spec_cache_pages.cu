@@ -5,7 +5,7 @@
 // gets how many pages off the stack) and a pass over the pages held, a few
 // kilobytes, and every order that a caller can see is fixed by request and
 // page numbers, never by the order in which threads arrive.  64 requests of
-// 500 tokens, each forked twice: reserve 5 us, fork 7, release 8, all latency (a
+// 500 to 131 tokens, each forked twice: reserve 5 us, fork 7, release 8, all latency (a
 // launch, the scan's barriers, dependent reads of table and counts).  What costs
 // bandwidth, the copy of a forked request's last partial page in every layer
 // and head, is a second kernel over the whole device.
@@ -255,8 +255,9 @@ __global__ void __launch_bounds__(kPageThreads) cache_fork_kernel(const CachePag
 // A CTA copies one fork's rows in a few (layer, head) blocks: four runs a block,
 // codes in 16-byte pieces and scales a row at a time, a piece of each of kBlocks
 // blocks in flight a thread.  It may be launched while the fork's decisions are
-// still being made.  128 forks at 500 tokens, 32 layers, 8 heads of 128 (301 MB read
-// and written): 62 us, 4.9 TB/s; one block in flight a thread is slower.
+// still being made.  128 forks at 500 to 131 tokens (0 to 63 rows each), 32 layers, 8 heads
+// of 128, 301 MB read and written: 53 us, 5.7 TB/s, reads in flight; one block in flight a
+// thread is slower.
 constexpr int kBlocks = 2;
 
 template <int D>

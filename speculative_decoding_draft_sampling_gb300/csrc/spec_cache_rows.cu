@@ -17,8 +17,8 @@
 // 1/(7 * 64) of it away from one, and is rounded to 13 bits first.
 //
 // Append and read move 4 bytes of codes or 16 of values a thread with four heads
-// in flight.  8 prompts of 8192 tokens, 8 heads of 128 (268 MB of bf16, 75 MB of
-// cache), take 62 us to append (5.5 TB/s) and 55 to read (6.3).  Reading is bound by
+// in flight.  8 prompts of 8192 tokens each, 8 heads of 128 (268 MB of bf16, 75 MB of
+// cache), take 62 us to append (5.6 TB/s) and 54 to read (6.3).  Reading is bound by
 // HBM; writing by its instructions as well (four fifths of the issue slots), so its
 // products come in pairs and its addresses by steps (4 us).  Eight heads in
 // flight cost 8 % more, two 3 %; registers cut for more warps an SM cost 8 % too.
@@ -31,8 +31,8 @@ namespace spec {
 
 namespace {
 
-// Append, then read of those prompts: 100 us at 128 threads; at 64 the same, at 256 4
-// more, at 512 10.
+// Append, then read of 8 prompts of 8192 to 4608 tokens (of 8192 rows given): 101 us at
+// 128 threads; at 64 the same, at 256 4 more, at 512 10.
 constexpr int kRowThreads = 128;
 
 // Eight bf16 of a row into registers, as four words.
