@@ -12,7 +12,8 @@ Inputs and outputs may be CUDA tensors or pinned host tensors
 (``tensor.pin_memory()``): the kernels read pinned host arrays in place over
 the CPU-GPU link, so a call on host-resident logits moves only the rows it
 reads (rows past a rejection stay on the host).  Outputs that the call
-allocates, and the workspace, are on the current CUDA device.
+allocates, and the workspace, are on the current CUDA device; with `stream`
+given they belong to that stream, as under `torch.cuda.stream(stream)`.
 
 Functions (same names as the C entry points, without the ``spec_`` prefix):
   verify_chain   chain speculative sampling (accept min(1,p/q), residual, bonus)
@@ -27,6 +28,7 @@ Functions (same names as the C entry points, without the ``spec_`` prefix):
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from dataclasses import dataclass
@@ -123,6 +125,18 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _on_stream(call):
+    """With stream= given, that stream is the current one while the call lasts,
+    so that what the call allocates and fills belongs to it."""
+    @functools.wraps(call)
+    def on(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        with torch.cuda.stream(stream):
+            return call(*args, stream=stream, **kw)
+    return on
+
+
 def _cuda(t: torch.Tensor, name: str, dtype=None):
     """A CUDA tensor, or a pinned host tensor that the kernels read (or write)
     in place through its device mapping."""
@@ -188,6 +202,7 @@ class ChainResult:
     ws: torch.Tensor
 
 
+@_on_stream
 def verify_chain(logits, q, draft, uniforms, temperature: float, top_k: int = 0, *,
                  k_per_req=None, l_row_off=None, q_row_off=None, diag: bool = False,
                  out: Optional[ChainResult] = None, ws: Optional[torch.Tensor] = None,
@@ -269,6 +284,7 @@ class GreedyResult:
     ws: torch.Tensor
 
 
+@_on_stream
 def verify_greedy(logits, draft, *, k_per_req=None, l_row_off=None, out: Optional[GreedyResult] = None,
                   ws: Optional[torch.Tensor] = None, stream=None) -> GreedyResult:
     """Greedy argmax-match verification.  Layouts as in verify_chain."""
@@ -324,6 +340,7 @@ class Tree:
     ws: torch.Tensor
 
 
+@_on_stream
 def tree_build(q, budget: int, *, out: Optional[Tree] = None, ws: Optional[torch.Tensor] = None,
                stream=None) -> Tree:
     """DDTree best-first tree over per-depth marginals q [B, L, V] fp32."""
@@ -378,6 +395,7 @@ def eagle_state(B: int, G: int, device) -> EagleState:
     return st
 
 
+@_on_stream
 def eagle_expand(q, state: EagleState, front, num_front, K2: int, Fn: int, *, front_out=None,
                  num_front_out=None, status=None, ws: Optional[torch.Tensor] = None, stream=None):
     """One EAGLE-2 expansion step (page §4): q [B, F, V] fp32 holds the draft's
@@ -415,6 +433,7 @@ def eagle_expand(q, state: EagleState, front, num_front, K2: int, Fn: int, *, fr
     return front_out, num_front_out, status
 
 
+@_on_stream
 def eagle_rerank(state: EagleState, budget: int, *, out: Optional[Tree] = None, stream=None) -> Tree:
     """The EAGLE-2 verification tree (page §4): the root and the budget-1
     best generated nodes, in the layout tree_build returns."""
@@ -448,6 +467,7 @@ class TreeWalk:
     ws: torch.Tensor
 
 
+@_on_stream
 def verify_tree(logits, token, parent, num_nodes, max_depth: int, *, out: Optional[TreeWalk] = None,
                 ws: Optional[torch.Tensor] = None, stream=None) -> TreeWalk:
     """Greedy tree walk over target logits [B, N, V] (fp32 or bf16)."""
@@ -480,6 +500,7 @@ def verify_tree(logits, token, parent, num_nodes, max_depth: int, *, out: Option
     return out
 
 
+@_on_stream
 def verify_tree_sample(logits, token, parent, num_nodes, uniforms, max_depth: int, temperature: float,
                        top_k: int = 0, *, out: Optional[TreeWalk] = None, ws: Optional[torch.Tensor] = None,
                        stream=None) -> TreeWalk:
@@ -562,6 +583,7 @@ class AdaptiveLen:
     q_row_off: torch.Tensor  # [B+1] int32
 
 
+@_on_stream
 def adaptive_len(conf, a: float, b: float, *, cost=None, out: Optional[AdaptiveLen] = None,
                  stream=None) -> AdaptiveLen:
     """DSpark verify length from conditional confidences conf [B, Kmax] fp32;
