@@ -161,14 +161,20 @@ def _ldt(t: torch.Tensor) -> int:
 
 
 _ws_cache: dict = {}
+_ws_outgrown: list = []     # never freed: a captured graph may still work in one
 
 
 def workspace(nbytes: int, device) -> torch.Tensor:
     """A cached device scratch buffer of at least ``nbytes`` bytes (one per
-    device); calls on one stream may share it, concurrent calls must not."""
+    device); calls on one stream may share it, concurrent calls must not.  It
+    doubles at least when it grows, so that what was outgrown adds up to less
+    than what is in use."""
     key = torch.device(device).index if torch.device(device).index is not None else torch.cuda.current_device()
     buf = _ws_cache.get(key)
     if buf is None or buf.numel() < nbytes:
+        if buf is not None:
+            _ws_outgrown.append(buf)
+            nbytes = max(nbytes, 2 * buf.numel())
         buf = torch.empty(max(nbytes, 1 << 12), dtype=torch.uint8, device=torch.device("cuda", key))
         _ws_cache[key] = buf
     return buf

@@ -62,3 +62,36 @@ def test_outputs_belong_to_the_given_stream():
     for name, tensors in got.items():
         assert all(stream_of(t) == side.cuda_stream for t in tensors), name
         assert torch.equal(tensors[0], want[name][0]), name      # tokens, lengths, nodes
+
+
+@pytest.fixture
+def fresh_workspaces(monkeypatch):
+    monkeypatch.setattr(sv, "_ws_cache", {})
+
+
+def test_outgrown_workspaces_are_nobody_elses(fresh_workspaces):
+    at, size = sv.workspace(5 << 20, DEV).data_ptr(), 5 << 20
+    assert sv.workspace(6 << 20, DEV).numel() >= 10 << 20
+    others = [torch.empty(n, dtype=torch.uint8, device=DEV) for n in (5 << 20, 1 << 20, 4 << 20, 5 << 20, 2 << 20)]
+    assert all(x.data_ptr() + x.numel() <= at or x.data_ptr() >= at + size for x in others)
+
+
+def test_graph_keeps_its_workspace(fresh_workspaces):
+    """A captured call, then one that needs more, then others that take what is free."""
+    g = torch.Generator(device=DEV).manual_seed(2)
+    logits = torch.rand((2, 5, 4000), device=DEV, generator=g)
+    draft = torch.randint(0, 4000, (2, 4), device=DEV, dtype=torch.int32, generator=g)
+    r = sv.verify_greedy(logits, draft)
+    want = (r.tokens.clone(), r.num_accepted.clone())
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        sv.verify_greedy(logits, draft, out=sv.GreedyResult(r.tokens, r.num_accepted, r.status, None))
+    sv.workspace(64 << 20, DEV)
+    junk = [torch.full((n,), 255, dtype=torch.uint8, device=DEV) for n in (1 << 12, 1 << 16, 1 << 20, 2 << 20) for _ in range(8)]
+    for _ in range(3):
+        r.tokens.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(r.tokens, want[0]) and torch.equal(r.num_accepted, want[1])
+    assert all(bool((x == 255).all()) for x in junk)
