@@ -104,8 +104,8 @@ spec_status spec_cache_read(
  * Outputs: out bf16 [B, n, q_heads, D] contiguous: softmax over the seen keys
  *   times V (sums in fp32; the weights meet V in bf16 and are divided by the sum
  *   of what they were rounded to); lse NULL or fp32 [B, n, q_heads]: natural log
- *   of the softmax's denominator, of weights before that rounding.  Rows that see nothing, and rows i >= num_rows[b], are 0 with
- *   lse = -inf.  Positions past the last drafted row, and context that lies
+ *   of the softmax's denominator, of weights before that rounding.  Rows that
+ *   see nothing, and rows i >= num_rows[b], are 0 with lse = -inf.  Positions past the last drafted row, and context that lies
  *   outside every row's window, contribute nothing whatever the cache holds
  *   there.  Scales of all other positions must be finite, as spec_cache_append
  *   writes them.
